@@ -261,6 +261,63 @@ VIDATTN_API int vidattn_fwd_noalloc(const void* q, const void* k, const void* v,
                                     int B, int H, int S_q, int S_kv, int D, float scale,
                                     vidattn_stream_t stream);
 
+/*
+ * vidattn_bwd — the gradient of vidattn_fwd_ex: from the gradients of its out
+ * and lse, those of its q, k and v.  The softmax weights are recomputed tile
+ * by tile from q, k and the forward's lse (after FlashAttention's backward
+ * pass, the vidax paper's reference [2]); nothing quadratic in S is stored:
+ *
+ *   with P_ij = exp(scale * q_i . k_j - lse_i) for the keys j visible to query
+ *   i (0 for the others), dP_ij = dout_i . v_j and
+ *   delta_i = dout_i . out_i - dlse_i:
+ *     dv_j = sum_i P_ij dout_i
+ *     dq_i = scale * sum_j P_ij (dP_ij - delta_i) k_j
+ *     dk_j = scale * sum_i P_ij (dP_ij - delta_i) q_i
+ *
+ *   q, k, v, seg_q, seg_kv, B, H, S_q, S_kv, D, scale
+ *           as given to the forward (same layouts, same rules)
+ *   out, lse  as the forward returned them, bf16 [B,H,S_q,D], fp32 [B,H,S_q]
+ *   dout    bf16 [B,H,S_q,D]: gradient of out, contiguous, 16-byte aligned
+ *   dlse    fp32 [B,H,S_q]: gradient of lse, or NULL for zero
+ *   dq      bf16 [B,H,S_q,D], written; dk, dv bf16 [B,H,S_kv,D], written.
+ *           None may overlap an input or another output.  A query that sees
+ *           no key gets dq = 0; a key no query sees gets dk = dv = 0.
+ *   flags   0 or VIDATTN_CAUSAL (as the forward's), and VIDATTN_SPLIT_KV(n),
+ *           1 <= n <= 64: the tiles that each key block (for dk, dv) and each
+ *           query block (for dq) visits are cut into n ranges whose partial
+ *           sums are added in order; 0 lets the library choose.
+ *   workspace  vidattn_bwd_workspace(...) bytes of device memory, 256-byte
+ *           aligned, owned by the caller: written and read by this call only;
+ *           free once the stream has passed it.  Calls that may overlap on
+ *           the GPU, or graphs that may run at the same time, need one each.
+ *
+ * Every value must be finite, padding's too (an infinity or a NaN in a token
+ * may reach the gradients of all tokens of its 128-token tile, as in the
+ * forward).  Arithmetic: products of bf16 values accumulated in fp32; P, dP,
+ * delta and dS = P (dP - delta) in fp32; P and dS are rounded to bf16 where
+ * they enter a product (they are operands of the tensor core); each gradient
+ * is summed in fp32 in a fixed order and rounded once to bf16.  The same
+ * inputs give bitwise the same gradients.
+ *
+ * Two kernels (row statistics; the gradients), and a third that adds the
+ * ranges when units are split.  No allocation, no library scratch: after a
+ * first call on a device it can be captured into a graph.  Errors: as
+ * vidattn_fwd; a workspace that is too small is VIDATTN_ERR_SCRATCH_LIMIT.
+ * S_q == 0 or S_kv == 0: the gradients that exist are set to zero.
+ */
+VIDATTN_API int vidattn_bwd(const void* q, const void* k, const void* v, const void* out,
+                            const void* dout, const float* lse, const float* dlse,
+                            const int32_t* seg_q, const int32_t* seg_kv,
+                            void* dq, void* dk, void* dv,
+                            int B, int H, int S_q, int S_kv, int D, float scale, int flags,
+                            void* workspace, int64_t workspace_bytes, vidattn_stream_t stream);
+
+/* Bytes of workspace a vidattn_bwd call with these arguments needs (has_ids:
+ * nonzero when segment ids are given), or -1 for arguments it refuses.  Pure
+ * host logic; no CUDA call. */
+VIDATTN_API int64_t vidattn_bwd_workspace(int has_ids, int B, int H, int S_q, int S_kv, int D,
+                                          int flags);
+
 #define VIDATTN_ROPE_HALF_SPLIT 1   /* pair feature k with k + d/2 instead of 2k with 2k+1 */
 
 /*

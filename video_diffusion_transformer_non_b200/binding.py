@@ -7,6 +7,7 @@ fails, these functions raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -70,6 +71,10 @@ def load_library():
     lib.vidattn_rope3d.argtypes = [p, p, p, p, i32, i32, i32, i32, i64, i64, i64,
                                    i32, i32, i32, i32, i32, i32, i32, f64, i32, p]
     lib.vidattn_rope3d.restype = i32
+    lib.vidattn_bwd.argtypes = [p] * 12 + [i32, i32, i32, i32, i32, f32, i32, p, i64, p]
+    lib.vidattn_bwd.restype = i32
+    lib.vidattn_bwd_workspace.argtypes = [i32] * 7
+    lib.vidattn_bwd_workspace.restype = i64
     lib.vidattn_version.argtypes = []
     lib.vidattn_version.restype = ctypes.c_char_p
     _lib = lib
@@ -253,6 +258,74 @@ def attention(q, k, v, seg_q=None, seg_kv=None, scale=None, stream=None, causal=
     if st != VIDATTN_OK:
         raise RuntimeError(f"vidattn_fwd failed: {status_string(st)} ({st})")
     return out, lse
+
+
+def vidattn_bwd(q, k, v, out, dout, lse, dlse, seg_q, seg_kv, dq, dk, dv, B, H, S_q, S_kv, D,
+                scale, flags, workspace, workspace_bytes, stream=None) -> int:
+    """Enqueue the attention's backward pass on ``stream``.  Returns the status."""
+    return load_library().vidattn_bwd(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse), _ptr(dlse), _ptr(seg_q),
+        _ptr(seg_kv), _ptr(dq), _ptr(dk), _ptr(dv), int(B), int(H), int(S_q), int(S_kv), int(D),
+        float(scale), int(flags), _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def bwd_workspace(has_ids, B, H, S_q, S_kv, D, flags=0) -> int:
+    """Bytes of workspace a vidattn_bwd call needs (-1: arguments it refuses)."""
+    return load_library().vidattn_bwd_workspace(int(bool(has_ids)), int(B), int(H), int(S_q),
+                                                int(S_kv), int(D), int(flags))
+
+
+@contextlib.contextmanager
+def _on(tensor, stream):
+    """Makes the tensor's device current, and allocations belong to the stream
+    the work goes to (the current stream of that device by default); yields
+    that stream's handle."""
+    import torch
+    with torch.cuda.device(tensor.device):
+        if stream is None:
+            yield torch.cuda.current_stream().cuda_stream
+            return
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=tensor.device) if stream \
+                else torch.cuda.default_stream(tensor.device)
+        if stream.device != tensor.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {tensor.device}")
+        with torch.cuda.stream(stream):
+            yield stream.cuda_stream
+
+
+def attention_bwd(dout, q, k, v, out, lse, seg_q=None, seg_kv=None, scale=None, causal=False,
+                  dlse=None, stream=None, n_split=0):
+    """The gradients (dq, dk, dv) of ``attention``: dout is the gradient of its
+    out, dlse (or None) that of its lse; out and lse are what it returned, the
+    rest what it was given.  dout: bf16 [B,H,S_q,D] contiguous; dlse: fp32
+    [B,H,S_q].  n_split forces the split of long units (0: the library's
+    choice).  Returns bf16 tensors of the shapes of q, k, v; raises on error."""
+    import torch
+    _check_qkv(q, k, v)
+    B, H, S_q, D = q.shape
+    S_kv = k.shape[2]
+    _check_tensors(dict(q=q, dout=dout, out=out), torch.bfloat16, ndim=4)
+    _check_tensors(dict(lse=lse, dlse=dlse), torch.float32, ndim=3)
+    for name, t, shape in (("dout", dout, (B, H, S_q, D)), ("out", out, (B, H, S_q, D)),
+                           ("lse", lse, (B, H, S_q)), ("dlse", dlse, (B, H, S_q))):
+        if t is not None and tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {shape} (is {tuple(t.shape)})")
+    if lse.device != q.device:
+        raise ValueError(f"lse is on {lse.device}, q on {q.device}")
+    _check_per_token("seg_q", seg_q, "seg_kv", seg_kv, B, S_q, S_kv, q.device)
+    if scale is None:
+        scale = D ** -0.5
+    flags = (VIDATTN_CAUSAL if causal else 0) | VIDATTN_SPLIT_KV(n_split)
+    n = bwd_workspace(seg_q is not None, B, H, S_q, S_kv, D, flags)
+    with _on(q, stream) as handle:
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        ws = torch.empty(max(n, 0), dtype=torch.uint8, device=q.device)
+        st = vidattn_bwd(q, k, v, out, dout, lse, dlse, seg_q, seg_kv, dq, dk, dv, B, H, S_q, S_kv,
+                         D, scale, flags, ws if n > 0 else None, n, handle)
+    if st != VIDATTN_OK:
+        raise RuntimeError(f"vidattn_bwd failed: {status_string(st)} ({st})")
+    return dq, dk, dv
 
 
 VIDATTN_ROPE_HALF_SPLIT = 1

@@ -21,7 +21,9 @@ OUT = os.path.join(CSRC, "libvidattn.so")
 PROBES_OUT = os.path.join(CSRC, "libvidattn_probes.so")
 # (output, sources, dependencies)
 TARGETS = [
-    (OUT, ["vidattn.cu"], ["vidattn.cu", "fwd_kernel.cuh", "classify.cuh", "ptx.cuh", "rope3d.cuh"]),
+    (OUT, ["vidattn.cu", "bwd.cu"],
+     ["vidattn.cu", "fwd_kernel.cuh", "classify.cuh", "ptx.cuh", "rope3d.cuh", "internal.h",
+      "bwd.cu", "bwd_kernel.cuh"]),
     # unit probes of the kernel's tensor-core steps, used only by the GPU tests
     (PROBES_OUT, ["probes.cu"], ["probes.cu", "fwd_kernel.cuh", "ptx.cuh"]),
 ]
@@ -51,7 +53,7 @@ def build(force: bool = False, ptxas_verbose: bool = False, extra: list[str] | N
         if not force and not needs_build(out, deps):
             continue
         tmp = out + f".tmp{os.getpid()}"
-        cmd = [nvcc_path(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared",
+        cmd = [nvcc_path(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "--threads", "0",
                "-Xcompiler", "-fPIC,-fvisibility=hidden", "-cudart", "static",
                "-I", os.path.join(ROOT, "include"), "-o", tmp]
         if ptxas_verbose:
@@ -69,7 +71,8 @@ def build_trace() -> str:
     tmp = TRACE_OUT + f".tmp{os.getpid()}"
     cmd = [nvcc_path(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared",
            "-Xcompiler", "-fPIC,-fvisibility=hidden", "-cudart", "static", "-DVIDATTN_TRACE",
-           "-I", os.path.join(ROOT, "include"), "-o", tmp, os.path.join(CSRC, "vidattn.cu")]
+           "-I", os.path.join(ROOT, "include"), "-o", tmp,
+           *(os.path.join(CSRC, s) for s in TARGETS[0][1])]
     subprocess.run(cmd, check=True)
     os.replace(tmp, TRACE_OUT)
     return TRACE_OUT

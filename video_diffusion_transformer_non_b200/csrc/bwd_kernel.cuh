@@ -1,0 +1,774 @@
+// Backward pass of the masked attention (fwd_kernel.cuh) for sm_100a.
+//
+// With P_ij = exp(scale q_i.k_j - lse_i) on the visible pairs (0 elsewhere),
+// recomputed tile by tile from q, k and the forward's lse, and
+// delta_i = dout_i.out_i - dlse_i:
+//
+//   dV = P^T dO      dP = dO V^T      dS = P (dP - delta)
+//   dQ = scale dS K  dK = scale dS^T Q
+//
+// Two kinds of work units run in one launch.  A KV unit owns 128 keys, walks
+// the query tiles that see them and keeps dK and dV in tensor memory (four
+// products a tile pair: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO,
+// dK += dS^T Q); a Q unit owns 128 queries, walks their key tiles and keeps dQ
+// (three products: S, dP, dQ += dS K).  Recomputing S and dP in both costs
+// 7 products where 5 would do, but every gradient is summed by one CTA in a
+// fixed order: no atomics, no fp32 dQ in global memory, the same bits every
+// time.  P and dS go from registers straight to tensor memory, as the A
+// operand of the product that consumes them, and never touch shared memory.
+//
+// 384 threads: warps 0-7 compute P and dS (warp w holds TMEM lanes
+// 32 (w % 4) + [0, 32), columns 64 (w / 4) + [0, 64) of each score tile), warp
+// 8 issues the tcgen05.mma, warp 9 the TMA loads, warps 10-11 only help to
+// list the visited tiles.
+#pragma once
+#include <climits>
+#include <cstdint>
+#include <cuda.h>
+
+#include "fwd_kernel.cuh"
+#include "ptx.cuh"
+
+namespace vidattn {
+
+constexpr int kBwdThreads = 384;
+constexpr int kBwdMaxListed = 4096;   // visited tiles listed in shared memory (with ids)
+constexpr int kBwdMaskBit = 1 << 15;
+
+struct BwdParams {
+  // per 128-row query tile: -lse * log2(e) (row sees nothing or is past S_q:
+  // -inf, so its P is 0) and -delta, fp32 [B*H][n_q_tiles][2][128]
+  const float* stats;
+  const int32_t* seg_q;     // [B,S_q] or null
+  const int32_t* seg_kv;    // [B,S_kv] or null
+  const int4* q_sum;        // ids: [B,n_q_tiles] {min,max,uniform,0}, or null
+  const int4* kv_sum;       // [B,n_kv_tiles]
+  uint16_t* dq;             // bf16 [B,H,S_q,D]
+  uint16_t* dk;             // bf16 [B,H,S_kv,D]
+  uint16_t* dv;
+  // split units: fp32 partial sums [n_kv_split][2][B*H][S_kv][D] (dK then dV,
+  // dK unscaled) and [n_q_split][B*H][S_q][D], added up by bwd_combine_kernel
+  float* part_kv;
+  float* part_q;
+  int* err;                 // device error word
+  int BH, H, S_q, S_kv;
+  int n_q_tiles, n_kv_tiles;
+  int n_kv_split, n_q_split;
+  int n_kv_units;           // B*H*n_kv_tiles*n_kv_split, launched first
+  int causal, causal_off;
+  float c;                  // scale * log2(e)
+  float scale;
+};
+
+template <int D>
+struct BwdCfg {
+  static constexpr int kSub = D / 64;
+  static constexpr int kSubBytes = 128 * 128;
+  static constexpr int kTileBytes = kSub * kSubBytes;
+  static constexpr int kStages = 2;
+  // two stationary tiles, then kStages pairs of moving tiles
+  static constexpr int kOffFixed = 0;
+  static constexpr int kOffRingA = 2 * kTileBytes;
+  static constexpr int kOffRingB = kOffRingA + kStages * kTileBytes;
+  static constexpr int kOffStats = kOffRingB + kStages * kTileBytes;   // [kStages][2][128] fp32
+  static constexpr int kStatBytes = 2 * 128 * 4;
+  static constexpr int kOffBar = kOffStats + kStages * kStatBytes;
+  // fixed_full[2] a_full[S] a_empty[S] b_full[S] b_empty[S] s_full s_free
+  // p_full dp_full ds_full ds_free[2] done
+  static constexpr int kNumBars = 2 + 4 * kStages + 8;
+  static constexpr int kOffMisc = kOffBar + 8 * kNumBars;   // tmem addr, abort flag, counts
+  static constexpr int kOffList = (kOffMisc + 16 + 13 * 4 + 127) & ~127;
+  static constexpr int kSmemBytes = kOffList + 2 * kBwdMaxListed + 1024;   // + alignment slack
+  static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory on sm_100");
+  static constexpr uint32_t kTmemCols = 512;
+  // KV units: dV [0,D), dK [128,128+D), S/P [256,384), dP/dS [384,512).
+  // Q units: dQ [0,D), dS buffers [128,192) and [192,256), S [256,384), dP [384,512).
+  static constexpr uint32_t kTmemAcc0 = 0, kTmemAcc1 = 128, kTmemDS = 128, kTmemS = 256,
+                            kTmemDP = 384;
+  static constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);
+  static constexpr uint32_t kIdescAcc = idesc_bf16_f32(128, D, 0, 1);
+};
+
+// D[128 x 128] = A[128 x D] B[128 x D]^T, both K-major tiles in shared memory.
+template <int D>
+__device__ __forceinline__ void bwd_issue_score(uint32_t d_tmem, uint32_t sA, uint32_t sB) {
+  using C = BwdCfg<D>;
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint32_t off = (kk / 4) * C::kSubBytes + (kk % 4) * 32;
+    mma_ss_elect(d_tmem, smem_desc_sw128(sA + off, 16, 1024), smem_desc_sw128(sB + off, 16, 1024),
+                 C::kIdescS, kk > 0 ? 1u : 0u);
+  }
+}
+
+// Acc[128 x D] += A[128 x 128] B[128 x D]: A bf16 in tensor memory (rows
+// [0,64) of the contraction at a_lo, [64,128) at a_hi), B a shared tile.
+template <int D>
+__device__ __forceinline__ void bwd_issue_acc(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi,
+                                              uint32_t sB, bool accumulate) {
+  using C = BwdCfg<D>;
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk) {
+    const uint64_t b = smem_desc_sw128(sB + kk * 2048, C::kSubBytes, 1024);
+    const uint32_t a = (kk < 4) ? a_lo + kk * 8 : a_hi + (kk - 4) * 8;
+    mma_ts_elect(d_tmem, a, b, C::kIdescAcc, (accumulate || kk > 0) ? 1u : 0u);
+  }
+}
+
+// Untiled bulk copy into shared memory (16-byte aligned, size a multiple of 16).
+__device__ __forceinline__ void bulk_load_elect(uint32_t dst, const void* src, uint32_t bytes,
+                                                uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+      "\n\t}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// The other-side tiles a unit walks: positions [t0, t1) of its visit sequence
+// (first + each list entry, or first, first + 1, ...).
+struct BwdWalk {
+  const uint16_t* list;
+  int first, t0, t1;
+};
+
+// Is any pair of (query tile i, key tile j) hidden?  kv_side: the unit owns
+// the key tile (keys past S_kv are rows of its own that are never stored).
+template <bool kv_side>
+__device__ __forceinline__ bool bwd_pair_masked(const BwdParams& p, int b, int i, int j) {
+  bool masked = false;
+  if (!kv_side) masked = j == p.n_kv_tiles - 1 && (p.S_kv & 127) != 0;
+  if (p.causal) masked = masked || j * 128 + 127 > i * 128 + p.causal_off;
+  if (p.q_sum) {
+    const int4 a = __ldg(p.q_sum + static_cast<int64_t>(b) * p.n_q_tiles + i);
+    const int4 k = __ldg(p.kv_sum + static_cast<int64_t>(b) * p.n_kv_tiles + j);
+    masked = masked || !(a.z && k.z && a.x == k.x);
+  }
+  return masked;
+}
+
+// Which of the 64 columns [x0, x0 + 64) of a score tile row are visible, as
+// bits: lo <= column < hi, and the column's id equal to the row's.
+__device__ __forceinline__ uint64_t bwd_mask64(int x0, int lo, int hi, const int32_t* ids,
+                                               int n_ids, int my_id) {
+  uint64_t m = 0;
+  const int a = max(lo - x0, 0), e = min(hi - x0, 64);
+  if (a < e) m = (~0ull >> (64 - (e - a))) << a;
+  if (ids != nullptr) {
+    uint64_t eq = 0;
+    for (int x = 0; x < 64; ++x) {
+      const int col = x0 + x;
+      const int id = col < n_ids ? __ldg(ids + col) : 0;
+      if (id == my_id) eq |= 1ull << x;
+    }
+    m &= eq;
+  }
+  return m;
+}
+
+// One thread's 64 columns of a score tile row to probabilities: 2^(c s + off),
+// off the row's (kPerColumn false) or read per column from shared memory.  Of
+// every 16, the last kEmu on the FMA pipe.
+template <int kEmu, bool kPerColumn>
+__device__ __forceinline__ void bwd_probs(uint32_t taddr, float c, float off, const float* offs,
+                                          float (&pr)[64]) {
+  uint32_t r[2][32];
+  tmem_ld32(taddr, r[0]);
+  tmem_ld32(taddr + 32, r[1]);
+  tmem_ld_wait();
+  reg_fence(r[0]);
+  reg_fence(r[1]);
+  const float2 c2 = make_float2(c, c);
+#pragma unroll
+  for (int x = 0; x < 64; x += 4) {
+    float4 o = make_float4(off, off, off, off);
+    if (kPerColumn) o = *reinterpret_cast<const float4*>(offs + x);
+#pragma unroll
+    for (int y = 0; y < 4; y += 2) {
+      const int e = x + y;
+      const float2 arg = ffma2(make_float2(__uint_as_float(r[e >> 5][e & 31]),
+                                           __uint_as_float(r[e >> 5][(e & 31) + 1])),
+                               c2, y == 0 ? make_float2(o.x, o.y) : make_float2(o.z, o.w));
+      float2 v;
+      if ((e & 15) < 16 - kEmu) {
+        v.x = ex2(arg.x);
+        v.y = ex2(arg.y);
+      } else {
+        v = exp2_poly2(arg);
+      }
+      pr[e] = v.x;
+      pr[e + 1] = v.y;
+    }
+  }
+}
+
+// dS = P (dP - delta) of the same 64 columns, packed to bf16 pairs.
+template <bool kPerColumn>
+__device__ __forceinline__ void bwd_dscores(uint32_t taddr, float nd, const float* nds,
+                                            const float (&pr)[64], uint32_t (&pk)[32]) {
+  uint32_t r[2][32];
+  tmem_ld32(taddr, r[0]);
+  tmem_ld32(taddr + 32, r[1]);
+  tmem_ld_wait();
+  reg_fence(r[0]);
+  reg_fence(r[1]);
+#pragma unroll
+  for (int x = 0; x < 64; x += 4) {
+    float4 o = make_float4(nd, nd, nd, nd);
+    if (kPerColumn) o = *reinterpret_cast<const float4*>(nds + x);
+    const float oo[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+    for (int y = 0; y < 4; y += 2) {
+      const int e = x + y;
+      const float2 t = fadd2(make_float2(__uint_as_float(r[e >> 5][e & 31]),
+                                         __uint_as_float(r[e >> 5][(e & 31) + 1])),
+                             make_float2(oo[y], oo[y + 1]));
+      pk[e >> 1] = pack_bf16x2(pr[e] * t.x, pr[e + 1] * t.y);
+    }
+  }
+}
+
+// One row of an accumulator from tensor memory, times mul, to bf16 (out) or
+// to fp32 (part).  have: the accumulator was written (a tile was visited).
+template <int D>
+__device__ __forceinline__ void bwd_store_row(uint32_t taddr, bool have, bool row_valid, float mul,
+                                              uint16_t* out, float* part) {
+#pragma unroll 1
+  for (int kk = 0; kk < D / 32; ++kk) {
+    uint32_t o[32];
+    if (have) {
+      tmem_ld32(taddr + 32 * kk, o);
+      tmem_ld_wait();
+      reg_fence(o);
+    } else {
+#pragma unroll
+      for (int x = 0; x < 32; ++x) o[x] = 0u;
+    }
+    if (!row_valid) continue;
+    if (part) {
+      float4* dst = reinterpret_cast<float4*>(part + 32 * kk);
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        dst[x] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
+                             __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
+    } else {
+      uint32_t w[16];
+#pragma unroll
+      for (int x = 0; x < 16; ++x)
+        w[x] = pack_bf16x2(__uint_as_float(o[2 * x]) * mul, __uint_as_float(o[2 * x + 1]) * mul);
+      uint4* dst = reinterpret_cast<uint4*>(out + 32 * kk);
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        dst[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+    }
+  }
+}
+
+// One unit.  kKV: it owns key tile `own`; else query tile `own`.
+template <int D, int kEmu, bool kKV>
+__device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                                         const CUtensorMap& tm_v, const CUtensorMap& tm_do,
+                                         const BwdParams& p, uint32_t sbase, uint8_t* smem,
+                                         uint32_t tmem, int bh, int own, int split, int n_split) {
+  using C = BwdCfg<D>;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int b = bh / p.H;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  auto bar = [&](int i) { return sbase + C::kOffBar + 8 * i; };
+  auto fixed_full = [&](int i) { return bar(i); };
+  auto a_full = [&](int s) { return bar(2 + s); };
+  auto a_empty = [&](int s) { return bar(2 + C::kStages + s); };
+  auto b_full = [&](int s) { return bar(2 + 2 * C::kStages + s); };
+  auto b_empty = [&](int s) { return bar(2 + 3 * C::kStages + s); };
+  constexpr int kB0 = 2 + 4 * C::kStages;
+  const uint32_t s_full = bar(kB0), s_free = bar(kB0 + 1), p_full = bar(kB0 + 2),
+                 dp_full = bar(kB0 + 3), ds_full = bar(kB0 + 4), done = bar(kB0 + 7);
+  auto ds_free = [&](int i) { return bar(kB0 + 5 + i); };
+  const uint32_t sFix[2] = {sbase + C::kOffFixed, sbase + C::kOffFixed + C::kTileBytes};
+  auto sA = [&](int s) { return sbase + C::kOffRingA + s * C::kTileBytes; };
+  auto sB = [&](int s) { return sbase + C::kOffRingB + s * C::kTileBytes; };
+
+  // ---------------------------------------------- the tiles this unit visits
+  // without ids: a contiguous range; with ids: listed (up to kBwdMaxListed
+  // tiles; beyond, every tile of the range is walked and masked)
+  BwdWalk walk{nullptr, 0, 0, 0};
+  int end;
+  if (kKV) {
+    end = p.n_q_tiles;
+    if (p.causal) {   // the first query row that sees key own * 128
+      const int row = own * 128 - p.causal_off;
+      walk.first = row <= 0 ? 0 : min(row / 128, end);
+    }
+  } else {
+    end = p.n_kv_tiles;
+    if (p.causal) {   // one past the last key row own * 128 + 127 sees
+      const int last = min(own * 128 + 127, p.S_q - 1) + p.causal_off;
+      end = last < 0 ? 0 : min(end, last / 128 + 1);
+    }
+  }
+  int total = max(end - walk.first, 0);
+  if (p.q_sum != nullptr && total <= kBwdMaxListed) {
+    uint16_t* list = reinterpret_cast<uint16_t*>(smem + C::kOffList);
+    int* counts = reinterpret_cast<int*>(smem + C::kOffMisc + 16);   // [12]
+    const int4* mine = (kKV ? p.kv_sum : p.q_sum) +
+                       static_cast<int64_t>(b) * (kKV ? p.n_kv_tiles : p.n_q_tiles) + own;
+    const int4* other = (kKV ? p.q_sum : p.kv_sum) +
+                        static_cast<int64_t>(b) * (kKV ? p.n_q_tiles : p.n_kv_tiles);
+    const int4 me = __ldg(mine);
+    int base = 0;
+    for (int t0 = walk.first; t0 < end; t0 += kBwdThreads) {
+      const int t = t0 + int(threadIdx.x);
+      bool act = false, masked = false;
+      if (t < end) {
+        const int4 o = __ldg(other + t);
+        act = !(o.y < me.x || o.x > me.y);
+        masked = kKV ? bwd_pair_masked<kKV>(p, b, t, own) : bwd_pair_masked<kKV>(p, b, own, t);
+      }
+      const unsigned ballot = __ballot_sync(0xffffffffu, act);
+      if (lane == 0) counts[warp] = __popc(ballot);
+      __syncthreads();
+      int at = base;
+      for (int w = 0; w < kBwdThreads / 32; ++w) {
+        const int n = counts[w];
+        if (w < warp) at += n;
+        base += n;
+      }
+      if (act)
+        list[at + __popc(ballot & ((1u << lane) - 1u))] =
+            static_cast<uint16_t>((t - walk.first) | (masked ? kBwdMaskBit : 0));
+      __syncthreads();
+    }
+    walk.list = list;
+    total = base;
+  }
+  walk.t0 = int((int64_t(total) * split) / n_split);
+  walk.t1 = int((int64_t(total) * (split + 1)) / n_split);
+  const int n_tiles = walk.t1 - walk.t0;
+  auto tile_at = [&](int t) {
+    return walk.first + (walk.list ? walk.list[walk.t0 + t] & (kBwdMaskBit - 1) : walk.t0 + t);
+  };
+  auto masked_at = [&](int t, int tile) {
+    if (walk.list) return (walk.list[walk.t0 + t] & kBwdMaskBit) != 0;
+    return kKV ? bwd_pair_masked<kKV>(p, b, tile, own) : bwd_pair_masked<kKV>(p, b, own, tile);
+  };
+  auto par = [](int n) { return uint32_t(n / C::kStages) & 1u; };
+
+  if (warp == 9) {
+    // -------------------------------------------------------------- loads
+    // KV unit: K and V stay; ring A holds Q (and its row statistics), ring B
+    // dO.  Q unit: Q and dO stay; ring A holds K, ring B V.
+    const CUtensorMap* fixed_map[2] = {kKV ? &tm_k : &tm_q, kKV ? &tm_v : &tm_do};
+    const CUtensorMap* ring_map[2] = {kKV ? &tm_q : &tm_k, kKV ? &tm_do : &tm_v};
+    bool ok = true;
+    int n = 0;
+    for (; n < n_tiles && ok; ++n) {
+      const int st = n % C::kStages;
+      const int tile = tile_at(n);
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        if (n == 0) {
+          mbar_arrive_expect_tx_elect(fixed_full(which), C::kTileBytes);
+          for (int s = 0; s < C::kSub; ++s)
+            tma_load_3d_elect(sFix[which] + s * C::kSubBytes, fixed_map[which], fixed_full(which),
+                              s * 64, own * 128, bh);
+        }
+        const uint32_t full = which ? b_full(st) : a_full(st);
+        ok = warp_wait_phase(which ? b_empty(st) : a_empty(st), par(n) ^ 1u, abort_flag, p.err);
+        if (!ok) break;
+        const bool with_stats = kKV && which == 0;
+        mbar_arrive_expect_tx_elect(full, C::kTileBytes + (with_stats ? C::kStatBytes : 0));
+        const uint32_t dst = which ? sB(st) : sA(st);
+        for (int s = 0; s < C::kSub; ++s)
+          tma_load_3d_elect(dst + s * C::kSubBytes, ring_map[which], full, s * 64, tile * 128, bh);
+        if (with_stats)
+          bulk_load_elect(sbase + C::kOffStats + st * C::kStatBytes,
+                          p.stats + (static_cast<int64_t>(bh) * p.n_q_tiles + tile) * 256,
+                          C::kStatBytes, full);
+      }
+    }
+    if (!ok) {
+      // let the loads in flight land before the CTA can exit (every load of
+      // the last kStages positions; a position never issued runs out of time)
+      volatile int never = 0;
+      for (int k = max(0, n - 1 - C::kStages); k < n - 1; ++k) {
+        warp_wait_phase(a_full(k % C::kStages), par(k), &never, p.err);
+        warp_wait_phase(b_full(k % C::kStages), par(k), &never, p.err);
+      }
+      warp_wait_phase(a_full((n - 1) % C::kStages), par(n - 1), &never, p.err);
+      warp_wait_phase(fixed_full(0), 0, &never, p.err);
+      warp_wait_phase(fixed_full(1), 0, &never, p.err);
+    }
+    __syncwarp();
+  } else if (warp == 8) {
+    // -------------------------------------------------------- tensor core
+    const uint32_t tS = tmem + C::kTmemS, tDP = tmem + C::kTmemDP;
+    bool ok = true;
+    if (n_tiles > 0) {
+      ok = warp_wait_phase(fixed_full(0), 0, abort_flag, p.err) &&
+           warp_wait_phase(a_full(0), 0, abort_flag, p.err);
+      if (ok) {
+        tc_fence_after();
+        bwd_issue_score<D>(tS, sFix[0], sA(0));
+        mma_commit_elect(s_full);
+        ok = warp_wait_phase(fixed_full(1), 0, abort_flag, p.err) &&
+             warp_wait_phase(b_full(0), 0, abort_flag, p.err);
+      }
+      if (ok) {
+        tc_fence_after();
+        bwd_issue_score<D>(tDP, sFix[1], sB(0));
+        mma_commit_elect(dp_full);
+        if (!kKV) mma_commit_elect(b_empty(0));
+      }
+    }
+    for (int n = 0; n < n_tiles && ok; ++n) {
+      const int st = n % C::kStages, st1 = (n + 1) % C::kStages;
+      const bool more = n + 1 < n_tiles;
+      const uint32_t tp = uint32_t(n) & 1u;
+      if (kKV) {
+        // dV += P^T dO_n, S = K Q_{n+1}^T, dK += dS^T Q_n, dP = V dO_{n+1}^T: P
+        // lies over S and dS over dP, whose next product follows in order
+        if (more) ok = warp_wait_phase(a_full(st1), par(n + 1), abort_flag, p.err);
+        ok = ok && warp_wait_phase(p_full, tp, abort_flag, p.err);
+        if (!ok) break;
+        tc_fence_after();
+        bwd_issue_acc<D>(tmem + C::kTmemAcc0, tS, tS + 64, sB(st), n > 0);
+        mma_commit_elect(b_empty(st));
+        if (more) {
+          bwd_issue_score<D>(tS, sFix[0], sA(st1));
+          mma_commit_elect(s_full);
+          ok = warp_wait_phase(b_full(st1), par(n + 1), abort_flag, p.err);
+        }
+        ok = ok && warp_wait_phase(ds_full, tp, abort_flag, p.err);
+        if (!ok) break;
+        tc_fence_after();
+        bwd_issue_acc<D>(tmem + C::kTmemAcc1, tDP, tDP + 64, sA(st), n > 0);
+        mma_commit_elect(a_empty(st));
+        if (more) {
+          bwd_issue_score<D>(tDP, sFix[1], sB(st1));
+          mma_commit_elect(dp_full);
+        }
+      } else {
+        // S = Q K_{n+1}^T once S_n is in registers, dP = dO V_{n+1}^T once
+        // dP_n is, dQ += dS_n K_n
+        if (more) {
+          ok = warp_wait_phase(a_full(st1), par(n + 1), abort_flag, p.err) &&
+               warp_wait_phase(s_free, tp, abort_flag, p.err);
+          if (!ok) break;
+          tc_fence_after();
+          bwd_issue_score<D>(tS, sFix[0], sA(st1));
+          mma_commit_elect(s_full);
+          ok = warp_wait_phase(b_full(st1), par(n + 1), abort_flag, p.err);
+        }
+        ok = ok && warp_wait_phase(ds_full, tp, abort_flag, p.err);
+        if (!ok) break;
+        tc_fence_after();
+        if (more) {
+          bwd_issue_score<D>(tDP, sFix[1], sB(st1));
+          mma_commit_elect(dp_full);
+          mma_commit_elect(b_empty(st1));
+        }
+        const uint32_t tDS = tmem + C::kTmemDS + 64u * (n & 1);
+        bwd_issue_acc<D>(tmem + C::kTmemAcc0, tDS, tDS + 32, sA(st), n > 0);
+        mma_commit_elect(a_empty(st));
+        mma_commit_elect(ds_free(n & 1));
+      }
+    }
+    // every product issued has finished before the epilogue and the release
+    // of tensor memory
+    mma_commit_elect(done);
+    volatile int never = 0;
+    warp_wait_phase(done, 0, &never, p.err);
+    __syncwarp();
+  } else if (warp < 8) {
+    // --------------------------------------------------------- P and dS
+    const int half = warp >> 2;
+    const int r = ((warp & 3) << 5) + lane;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_off + C::kTmemS + 64u * half;
+    const uint32_t tDP = tmem + lane_off + C::kTmemDP + 64u * half;
+    const int row = own * 128 + r;   // this thread's key (KV) or query row
+    float nlse = 0.f, ndelta = 0.f;
+    if (!kKV) {
+      const float* st = p.stats + (static_cast<int64_t>(bh) * p.n_q_tiles + own) * 256 + r;
+      nlse = __ldg(st);
+      ndelta = __ldg(st + 128);
+    }
+    bool ok = true;
+    for (int n = 0; n < n_tiles; ++n) {
+      const int st = n % C::kStages;
+      const uint32_t tp = uint32_t(n) & 1u;
+      const int tile = tile_at(n);
+      const bool masked = masked_at(n, tile);
+      const float* stats = reinterpret_cast<const float*>(smem + C::kOffStats +
+                                                          st * C::kStatBytes) + 64 * half;
+      uint64_t vis = ~0ull;
+      if (masked) {
+        const int x0 = tile * 128 + 64 * half;   // first column's query (KV) or key
+        int lo = 0, hi = kKV ? p.S_q : p.S_kv;
+        if (p.causal) {
+          if (kKV) lo = row - p.causal_off;
+          else hi = min(hi, row + p.causal_off + 1);
+        }
+        const int32_t* ids = nullptr;
+        int my_id = 0;
+        if (p.q_sum) {
+          const int32_t* own_ids = kKV ? p.seg_kv : p.seg_q;
+          const int n_own = kKV ? p.S_kv : p.S_q;
+          ids = (kKV ? p.seg_q : p.seg_kv) + static_cast<int64_t>(b) * (kKV ? p.S_q : p.S_kv);
+          if (row < n_own) my_id = __ldg(own_ids + static_cast<int64_t>(b) * n_own + row);
+        }
+        vis = bwd_mask64(x0, lo, hi, ids, kKV ? p.S_q : p.S_kv, my_id);
+      }
+      if (kKV) {   // the statistics of this query tile have landed
+        ok = warp_wait_phase(a_full(st), par(n), abort_flag, p.err);
+        if (!ok) break;
+      }
+      ok = warp_wait_phase(s_full, tp, abort_flag, p.err);
+      if (!ok) break;
+      tc_fence_after();
+      float pr[64];
+      bwd_probs<kEmu, kKV>(tS, p.c, nlse, stats, pr);
+      if (masked) {
+#pragma unroll
+        for (int x = 0; x < 64; ++x) pr[x] = (vis >> x) & 1 ? pr[x] : 0.f;
+      }
+      uint32_t pk[32];
+      if (kKV) {
+#pragma unroll
+        for (int x = 0; x < 32; ++x) pk[x] = pack_bf16x2(pr[2 * x], pr[2 * x + 1]);
+        tmem_st32(tS, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(p_full);
+      } else {
+        tc_fence_before();
+        mbar_arrive(s_free);
+      }
+      ok = warp_wait_phase(dp_full, tp, abort_flag, p.err);
+      if (!ok) break;
+      tc_fence_after();
+      bwd_dscores<kKV>(tDP, ndelta, stats + 128, pr, pk);
+      if (kKV) {
+        tmem_st32(tDP, pk);
+      } else {
+        if (n >= 2) {   // dQ's product of two tiles ago has read this buffer
+          ok = warp_wait_phase(ds_free(n & 1), uint32_t((n >> 1) - 1) & 1u, abort_flag, p.err);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        tmem_st32(tmem + lane_off + C::kTmemDS + 64u * (n & 1) + 32u * half, pk);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(ds_full);
+    }
+    // ------------------------------------------------------------ epilogue
+    ok = ok && warp_wait_phase(done, 0, abort_flag, p.err);
+    if (ok) {
+      tc_fence_after();
+      const bool have = n_tiles > 0;
+      if (kKV) {   // one half writes dV, the other dK
+        const bool valid = row < p.S_kv;
+        const int64_t at = (static_cast<int64_t>(bh) * p.S_kv + row) * D;
+        float* part = nullptr;
+        if (n_split > 1)
+          part = p.part_kv + (int64_t(split) * 2 + (half ? 0 : 1)) * p.BH * p.S_kv * D + at;
+        if (half == 0)
+          bwd_store_row<D>(tmem + lane_off + C::kTmemAcc0, have, valid, 1.f, p.dv + at, part);
+        else
+          bwd_store_row<D>(tmem + lane_off + C::kTmemAcc1, have, valid, p.scale, p.dk + at, part);
+      } else if (half == 0) {
+        const int64_t at = (static_cast<int64_t>(bh) * p.S_q + row) * D;
+        float* part = nullptr;
+        if (n_split > 1) part = p.part_q + int64_t(split) * p.BH * p.S_q * D + at;
+        bwd_store_row<D>(tmem + lane_off + C::kTmemAcc0, have, row < p.S_q, p.scale, p.dq + at,
+                         part);
+      }
+    }
+  }
+}
+
+// One CTA per unit: the KV units (four products a tile pair, the longer ones)
+// first, each kind with the split fastest, then the tile, then (b, h): the
+// units of one head run close together and share its tiles in L2.  With the
+// causal limit the longest tiles of a head go first.
+template <int D, int kEmu>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    vidattn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q,
+                       const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ CUtensorMap tm_do, const BwdParams p) {
+  using C = BwdCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_base = smem_u32(smem_raw);
+  const uint32_t sbase = (raw_base + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - raw_base);
+  // a wait of an earlier CTA timed out: the results are already invalid
+  if (*reinterpret_cast<volatile int*>(p.err) != 0) return;
+
+  const int warp = threadIdx.x >> 5;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  if (threadIdx.x == 0) {
+    auto bar = [&](int i) { return sbase + C::kOffBar + 8 * i; };
+    constexpr int kB0 = 2 + 4 * C::kStages;
+    for (int i = 0; i < C::kNumBars; ++i) {
+      const bool many = i == kB0 + 1 || i == kB0 + 2 || i == kB0 + 4;   // s_free p_full ds_full
+      mbar_init(bar(i), many ? 256 : 1);
+    }
+    *reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4) = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+
+  int u = blockIdx.x;
+  if (u < p.n_kv_units) {
+    const int split = u % p.n_kv_split;
+    u /= p.n_kv_split;
+    bwd_unit<D, kEmu, true>(tm_q, tm_k, tm_v, tm_do, p, sbase, smem, tmem, u / p.n_kv_tiles,
+                            u % p.n_kv_tiles, split, p.n_kv_split);
+  } else {
+    u -= p.n_kv_units;
+    const int split = u % p.n_q_split;
+    u /= p.n_q_split;
+    const int t = u % p.n_q_tiles;
+    bwd_unit<D, kEmu, false>(tm_q, tm_k, tm_v, tm_do, p, sbase, smem, tmem, u / p.n_q_tiles,
+                             p.causal ? p.n_q_tiles - 1 - t : t, split, p.n_q_split);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Ahead of the main kernel, one CTA per 128-row tile: -lse log2(e) and -delta
+// of a query tile of one (b, h) (blocks [0, BH * n_q_tiles)), and, with ids,
+// the tile summaries {min, max, uniform, 0} of seg_q (by the blocks of head
+// 0) and seg_kv (the blocks behind).  delta = dout . out - dlse: one pass
+// over dout and out, 16 bytes a lane, D / 8 lanes a row.
+template <int D>
+__global__ void __launch_bounds__(256)
+    bwd_prepare_kernel(const uint16_t* __restrict__ out, const uint16_t* __restrict__ dout,
+                       const float* __restrict__ lse, const float* __restrict__ dlse,
+                       const int32_t* __restrict__ seg_q, const int32_t* __restrict__ seg_kv,
+                       float* __restrict__ stats, int4* __restrict__ q_sum,
+                       int4* __restrict__ kv_sum, int BH, int H, int S_q, int S_kv,
+                       int n_q_tiles, int n_kv_tiles) {
+  constexpr int kLanes = D / 8;
+  constexpr int kRows = 256 / kLanes;
+  const int tid = threadIdx.x;
+  const int64_t blk = blockIdx.x;
+  const int64_t n_stat = static_cast<int64_t>(BH) * n_q_tiles;
+  const int32_t* ids = nullptr;
+  int4* sum = nullptr;
+  int first = 0, len = 0;
+  if (blk < n_stat) {
+    const int bh = int(blk / n_q_tiles), tile = int(blk % n_q_tiles);
+    float* st = stats + blk * 256;
+    const int ch = tid % kLanes;
+#pragma unroll
+    for (int r0 = 0; r0 < 128; r0 += kRows) {
+      const int r = r0 + tid / kLanes;
+      const int row = tile * 128 + r;
+      float acc = 0.f;
+      const int64_t at = static_cast<int64_t>(bh) * S_q + row;
+      if (row < S_q) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(out + at * D) + ch);
+        const uint4 g = __ldg(reinterpret_cast<const uint4*>(dout + at * D) + ch);
+        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, gw[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          acc = fmaf(__uint_as_float(aw[x] << 16), __uint_as_float(gw[x] << 16), acc);
+          acc = fmaf(__uint_as_float(aw[x] & 0xffff0000u), __uint_as_float(gw[x] & 0xffff0000u),
+                     acc);
+        }
+      }
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+      if (ch == 0) {
+        float nl = -INFINITY, nd = 0.f;
+        if (row < S_q) {
+          const float l = __ldg(lse + at);
+          if (l != -INFINITY) nl = -l * 1.44269504088896341f;
+          nd = (dlse ? __ldg(dlse + at) : 0.f) - acc;
+        }
+        st[r] = nl;
+        st[128 + r] = nd;
+      }
+    }
+    if (seg_q == nullptr || bh % H != 0) return;
+    const int b = bh / H;
+    ids = seg_q + static_cast<int64_t>(b) * S_q;
+    sum = q_sum + static_cast<int64_t>(b) * n_q_tiles + tile;
+    first = tile * 128;
+    len = S_q;
+  } else {
+    const int64_t u = blk - n_stat;
+    const int b = int(u / n_kv_tiles), tile = int(u % n_kv_tiles);
+    ids = seg_kv + static_cast<int64_t>(b) * S_kv;
+    sum = kv_sum + static_cast<int64_t>(b) * n_kv_tiles + tile;
+    first = tile * 128;
+    len = S_kv;
+  }
+  if (tid >= 32) return;
+  int lo = INT_MAX, hi = INT_MIN;
+  for (int x = tid; x < 128; x += 32) {
+    if (first + x < len) {
+      const int id = __ldg(ids + first + x);
+      lo = min(lo, id);
+      hi = max(hi, id);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  if (tid == 0) *sum = make_int4(lo, hi, lo == hi ? 1 : 0, 0);
+}
+
+// out[i] = mul * sum over splits of part[s * stride + i], rounded to bf16; 4
+// values a thread, in split order.
+__device__ __forceinline__ void bwd_combine4(const float* part, int64_t stride, int n_split,
+                                             float mul, uint16_t* out, int64_t i) {
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < n_split; ++s) {
+    const float4 v = __ldcs(reinterpret_cast<const float4*>(part + s * stride + 4 * i));
+    a.x += v.x;
+    a.y += v.y;
+    a.z += v.z;
+    a.w += v.w;
+  }
+  reinterpret_cast<uint2*>(out)[i] =
+      make_uint2(pack_bf16x2(a.x * mul, a.y * mul), pack_bf16x2(a.z * mul, a.w * mul));
+}
+
+template <int kUnused>
+__global__ void __launch_bounds__(256)
+    bwd_combine_kernel(const float* __restrict__ part_kv, int n_kv_split, int64_t n_kv,
+                       const float* __restrict__ part_q, int n_q_split, int64_t n_q, float scale,
+                       uint16_t* __restrict__ dk, uint16_t* __restrict__ dv,
+                       uint16_t* __restrict__ dq) {
+  int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (n_kv_split > 1) {
+    if (i < n_kv / 4) return bwd_combine4(part_kv, 2 * n_kv, n_kv_split, scale, dk, i);
+    i -= n_kv / 4;
+    if (i < n_kv / 4) return bwd_combine4(part_kv + n_kv, 2 * n_kv, n_kv_split, 1.f, dv, i);
+    i -= n_kv / 4;
+  }
+  if (n_q_split > 1 && i < n_q / 4) bwd_combine4(part_q, n_q, n_q_split, scale, dq, i);
+}
+
+}  // namespace vidattn

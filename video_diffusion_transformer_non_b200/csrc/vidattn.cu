@@ -18,6 +18,7 @@
 #include "../../include/vidattn.h"
 #include "classify.cuh"
 #include "fwd_kernel.cuh"
+#include "internal.h"
 #include "rope3d.cuh"
 
 namespace vidattn {
@@ -178,6 +179,7 @@ int emu_index(int D) {
 }
 std::mutex g_mu;
 std::map<int, DeviceInfo> g_devices;
+int g_epoch = 0;   // counts vidattn_release calls (internal.h)
 
 struct Scratch {
   void* ptr = nullptr;
@@ -520,6 +522,24 @@ void rope_tables(RopeParams& p, int D, const int bands[3], double theta, bool ha
 }
 
 }  // namespace
+
+// What the library's other translation units share (internal.h).
+namespace host {
+int device(int* dev, int** err, int* sms) {
+  const int st = ensure_device(dev);
+  if (st != VIDATTN_OK) return st;
+  *err = device_error_word(*dev);
+  *sms = device_sms(*dev);
+  return VIDATTN_OK;
+}
+bool tensor_map(const void* ptr, int64_t BH, int64_t S, int D, CUtensorMap* out) {
+  return encode_bhsd(out, ptr, BH, S, D);
+}
+int epoch() {
+  std::lock_guard<std::mutex> lk(g_mu);
+  return g_epoch;
+}
+}  // namespace host
 }  // namespace vidattn
 
 using namespace vidattn;
@@ -972,6 +992,7 @@ VIDATTN_API void vidattn_release(void) {
   // up again by the next call, so a context created after this (say, after
   // cudaDeviceReset) never sees addresses of the old one.
   g_devices.clear();
+  ++g_epoch;
   g_noalloc_ptr.clear();
   cudaSetDevice(prev);
 }
