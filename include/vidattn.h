@@ -2,8 +2,11 @@
  * vidattn: the multi-head attention forward of video diffusion transformers,
  * on NVIDIA B200 (sm_100a) — bidirectional attention masked by segment ids
  * (vidattn_fwd), with an optional causal limit (vidattn_fwd_ex) or a 3D
- * neighbourhood window (vidattn_fwd_window) — and the 3D rotary embedding of
- * q and k ahead of it (vidattn_rope3d).
+ * neighbourhood window (vidattn_fwd_window) —, its backward pass
+ * (vidattn_bwd), and what comes ahead of it: the layer norm
+ * (vidattn_layernorm, vidattn_layernorm_bwd) and the 3D rotary embedding of q
+ * and k (vidattn_rope3d; vidattn_rope3d_scaled with the caller's frequencies,
+ * and its gradient).
  *
  * The base operation (vidax: A Unified JAX Framework for Video Generative Models on
  * Accelerator Meshes, §2 "3D RoPE, 3D VAEs, and flash attention": full
@@ -318,6 +321,72 @@ VIDATTN_API int vidattn_bwd(const void* q, const void* k, const void* v, const v
 VIDATTN_API int64_t vidattn_bwd_workspace(int has_ids, int B, int H, int S_q, int S_kv, int D,
                                           int flags);
 
+/* Element types of arrays that come in more than one. */
+#define VIDATTN_BF16 0
+#define VIDATTN_F32 1
+
+/*
+ * vidattn_layernorm — layer norm over the last axis (Ba, Kiros and Hinton,
+ * 2016): of q and k over each head ahead of the rotary embedding, or of the
+ * hidden state ahead of a block.
+ *
+ *   mean = sum_f x_f / N,  rstd = 1 / sqrt(sum_f (x_f - mean)^2 / N + eps),
+ *   y_f = (x_f - mean) rstd weight_f + bias_f
+ *
+ *   x        bf16 or fp32 (x_type: VIDATTN_BF16 or VIDATTN_F32), logical shape
+ *            [B,H,S,N], element (b,h,s,f) at x + b*x_strides[0] +
+ *            h*x_strides[1] + s*x_strides[2] + f; strides in elements, >= 0
+ *   weight, bias  [N] of param_type (bf16 or fp32), either may be NULL (1, 0)
+ *   y        as x, with strides of its own; its rows must not overlap.  x
+ *            itself with x's strides (in place), or memory apart from x.
+ *   mean, rstd  fp32 [B,H,S] contiguous, written; either may be NULL
+ *   B, H >= 1; S >= 0; 1 <= N <= 16384; B*H*S < 2^31; eps >= 0, finite.
+ *
+ * Any alignment of the type works; rows on 16-byte boundaries with N a
+ * multiple of 8 are the fast ones.  Arithmetic in fp32, the variance about the
+ * mean (not as a difference of squares), y rounded once.  One kernel, no
+ * allocation, no scratch.  Errors before anything is enqueued: NULL,
+ * MISALIGNED (to the type's size), BAD_SHAPE for the rest.
+ */
+VIDATTN_API int vidattn_layernorm(const void* x, const void* weight, const void* bias, void* y,
+                                  float* mean, float* rstd, int B, int H, int S, int N,
+                                  const int64_t* x_strides, const int64_t* y_strides, int x_type,
+                                  int param_type, double eps, vidattn_stream_t stream);
+
+/*
+ * vidattn_layernorm_bwd — its gradients: with xh = (x - mean) rstd and
+ * g = dy weight,
+ *
+ *   dx = rstd (g - mean(g) - xh mean(g xh)) over the features of a row,
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy.
+ *
+ *   dy, x    as the forward's y and x (x_type), strides of their own
+ *   mean, rstd  as the forward wrote them
+ *   weight   as given to the forward, or NULL
+ *   dx       as x, strides of its own, rows apart; x or dy itself with the
+ *            same strides, or memory apart from both
+ *   dweight, dbias  [N] of param_type, written; either may be NULL
+ *   workspace  vidattn_layernorm_bwd_workspace(...) bytes, 256-byte aligned,
+ *            the caller's, for this call alone until the stream has passed it;
+ *            NULL when dweight and dbias are NULL
+ *
+ * Sums in fp32 in a fixed order: the same inputs on the same device give the
+ * same bits.  S == 0 sets dweight and dbias to zero.  One kernel, and a second
+ * for dweight and dbias; no allocation.  Errors as vidattn_layernorm, and
+ * VIDATTN_ERR_SCRATCH_LIMIT for a workspace that is too small.
+ */
+VIDATTN_API int vidattn_layernorm_bwd(const void* dy, const void* x, const float* mean,
+                                      const float* rstd, const void* weight, void* dx,
+                                      void* dweight, void* dbias, int B, int H, int S, int N,
+                                      const int64_t* dy_strides, const int64_t* x_strides,
+                                      const int64_t* dx_strides, int x_type, int param_type,
+                                      void* workspace, int64_t workspace_bytes,
+                                      vidattn_stream_t stream);
+
+/* Bytes of workspace a vidattn_layernorm_bwd call of these sizes needs, or -1
+ * for sizes it refuses.  Pure host logic; no CUDA call. */
+VIDATTN_API int64_t vidattn_layernorm_bwd_workspace(int B, int H, int S, int N, int x_type);
+
 #define VIDATTN_ROPE_HALF_SPLIT 1   /* pair feature k with k + d/2 instead of 2k with 2k+1 */
 
 /*
@@ -373,6 +442,47 @@ VIDATTN_API int vidattn_rope3d(const void* q_in, const void* k_in, void* q_out, 
                                int T, int Hg, int Wg, int token_offset,
                                int d_t, int d_h, int d_w, double theta, int flags,
                                vidattn_stream_t stream);
+
+#define VIDATTN_ROPE_TRANSPOSE 2   /* turn by the negative angle: the gradient's rotation */
+
+/*
+ * vidattn_rope3d_scaled — vidattn_rope3d for volumes beyond the trained one
+ * and for training: the frequencies are the caller's, positions may be
+ * interpolated, the bands may cover a part of the head, the outputs may be
+ * strided, and the transposed rotation gives the gradient.
+ *
+ *   pair c of the bands (c counts the pairs of the t, the h and the w band in
+ *   that order) of a video token is turned by
+ *     a = coord * pos_scale[axis] * freqs[c]
+ *   and scaled:  (x, y) -> amplitude (x cos a - y sin a, x sin a + y cos a),
+ *   with VIDATTN_ROPE_TRANSPOSE  amplitude (x cos a + y sin a, -x sin a + y cos a):
+ *   applied to the gradients of q_out and k_out it gives those of q_in and
+ *   k_in.  Features behind the bands and tokens outside the video are copied
+ *   bit for bit, without the amplitude.
+ *
+ *   freqs      (d_t + d_h + d_w) / 2 host doubles, read before the call returns
+ *   pos_scale  3 host doubles (t, h, w): 1 keeps a coordinate, 1/f interpolates
+ *   amplitude  finite; 1 for a pure rotation
+ *   d_t, d_h, d_w  even, >= 0, at most D together; what is left of a head is
+ *              copied
+ *   in_strides, out_strides  3 strides each (batch, head, token) in elements,
+ *              multiples of 8, of q_in and k_in and of q_out and k_out; input
+ *              strides >= 0; output rows apart.  An output is its input (then
+ *              with the same strides) or memory apart from both inputs.
+ *   flags      VIDATTN_ROPE_HALF_SPLIT | VIDATTN_ROPE_TRANSPOSE
+ *   the rest   as vidattn_rope3d
+ *
+ * |coord * pos_scale * freq| must stay below 2^30 over the volume (angles are
+ * taken in fp64).  Arithmetic and errors as vidattn_rope3d: angles in fp64,
+ * sine and cosine and the rotation in fp32, one rounding.  One kernel, no
+ * allocation.
+ */
+VIDATTN_API int vidattn_rope3d_scaled(const void* q_in, const void* k_in, void* q_out,
+                                      void* k_out, int B, int H, int S, int D,
+                                      const int64_t* in_strides, const int64_t* out_strides,
+                                      int T, int Hg, int Wg, int token_offset, int d_t, int d_h,
+                                      int d_w, const double* freqs, const double* pos_scale,
+                                      double amplitude, int flags, vidattn_stream_t stream);
 
 /* A static, human-readable name for a status code. */
 VIDATTN_API const char* vidattn_status_string(int status);

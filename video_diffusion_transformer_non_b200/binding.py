@@ -75,6 +75,15 @@ def load_library():
     lib.vidattn_bwd.restype = i32
     lib.vidattn_bwd_workspace.argtypes = [i32] * 7
     lib.vidattn_bwd_workspace.restype = i64
+    lib.vidattn_layernorm.argtypes = [p] * 6 + [i32] * 4 + [p, p, i32, i32, f64, p]
+    lib.vidattn_layernorm.restype = i32
+    lib.vidattn_layernorm_bwd.argtypes = [p] * 8 + [i32] * 4 + [p, p, p, i32, i32, p, i64, p]
+    lib.vidattn_layernorm_bwd.restype = i32
+    lib.vidattn_layernorm_bwd_workspace.argtypes = [i32] * 5
+    lib.vidattn_layernorm_bwd_workspace.restype = i64
+    lib.vidattn_rope3d_scaled.argtypes = [p, p, p, p, i32, i32, i32, i32, p, p, i32, i32, i32, i32,
+                                          i32, i32, i32, p, p, f64, i32, p]
+    lib.vidattn_rope3d_scaled.restype = i32
     lib.vidattn_version.argtypes = []
     lib.vidattn_version.restype = ctypes.c_char_p
     _lib = lib
@@ -328,6 +337,140 @@ def attention_bwd(dout, q, k, v, out, lse, seg_q=None, seg_kv=None, scale=None, 
     return dq, dk, dv
 
 
+VIDATTN_BF16, VIDATTN_F32 = 0, 1
+
+
+def _strides(values):
+    return (ctypes.c_int64 * 3)(*values)
+
+
+def vidattn_layernorm(x, weight, bias, y, mean, rstd, B, H, S, N, x_strides, y_strides, x_type,
+                      param_type, eps, stream=None) -> int:
+    """Enqueue the layer norm on ``stream``.  Returns the status."""
+    return load_library().vidattn_layernorm(
+        _ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean), _ptr(rstd), int(B), int(H), int(S),
+        int(N), _strides(x_strides), _strides(y_strides), int(x_type), int(param_type), float(eps),
+        _stream(stream))
+
+
+def vidattn_layernorm_bwd(dy, x, mean, rstd, weight, dx, dweight, dbias, B, H, S, N, dy_strides,
+                          x_strides, dx_strides, x_type, param_type, workspace, workspace_bytes,
+                          stream=None) -> int:
+    """Enqueue the layer norm's gradients on ``stream``.  Returns the status."""
+    return load_library().vidattn_layernorm_bwd(
+        _ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dx), _ptr(dweight),
+        _ptr(dbias), int(B), int(H), int(S), int(N), _strides(dy_strides), _strides(x_strides),
+        _strides(dx_strides), int(x_type), int(param_type), _ptr(workspace), int(workspace_bytes),
+        _stream(stream))
+
+
+def layernorm_bwd_workspace(B, H, S, N, x_type) -> int:
+    """Bytes of workspace a vidattn_layernorm_bwd call needs (-1: sizes it refuses)."""
+    return load_library().vidattn_layernorm_bwd_workspace(int(B), int(H), int(S), int(N),
+                                                          int(x_type))
+
+
+def _type_code(t):
+    import torch
+    codes = {torch.bfloat16: VIDATTN_BF16, torch.float32: VIDATTN_F32}
+    if t not in codes:
+        raise ValueError(f"dtype must be bfloat16 or float32 (is {t})")
+    return codes[t]
+
+
+def _rows(name, t, shape=None):
+    """A tensor of 1 to 4 dims as rows of [B,H,S,N]: its last dim contiguous,
+    any strides for the others.  Returns (B, H, S, N), (sb, sh, ss)."""
+    if not 1 <= t.dim() <= 4:
+        raise ValueError(f"{name} must have 1 to 4 dims (has shape {tuple(t.shape)})")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)} (is {tuple(t.shape)})")
+    if t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError(f"the last dim of {name} must be contiguous")
+    pad = 4 - t.dim()
+    sizes = (1,) * pad + tuple(t.shape)
+    strides = (0,) * pad + tuple(t.stride())
+    return sizes, tuple(s if n > 1 else 0 for s, n in zip(strides[:3], sizes))
+
+
+def _check_norm(x, named, weight, bias):
+    """Common checks of layer_norm and layer_norm_bwd; returns the types."""
+    import torch
+    if not isinstance(x, torch.Tensor):
+        raise ValueError(f"x must be a torch tensor, not {type(x).__name__}")
+    x_type = _type_code(x.dtype)
+    _check_tensors(dict(x=x, **named), x.dtype, contiguous=False)
+    if weight is None and bias is None:
+        return x_type, VIDATTN_F32
+    p = weight if weight is not None else bias
+    if not isinstance(p, torch.Tensor):
+        raise ValueError(f"weight and bias must be torch tensors, not {type(p).__name__}")
+    p_type = _type_code(p.dtype)
+    _check_tensors(dict(weight=weight, bias=bias), p.dtype, ndim=1)
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None and (t.device != x.device or t.shape[0] != x.shape[-1]):
+            raise ValueError(f"{name} must be [{x.shape[-1]}] on {x.device} (is "
+                             f"{tuple(t.shape)} on {t.device})")
+    return x_type, p_type
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-6, out=None, stream=None):
+    """Layer norm over the last dim.  x: bf16 or fp32 of 1 to 4 dims, the last
+    contiguous, any other strides (the [B,S,H,D] projection's ``transpose(1, 2)``
+    view works); weight, bias: [N], bf16 or fp32, or None.  ``out=x`` works in
+    place.  Returns (y contiguous or out, mean, rstd), the statistics fp32 of
+    x's shape without its last dim; raises on error."""
+    import torch
+    x_type, p_type = _check_norm(x, dict(out=out), weight, bias)
+    (B, H, S, N), sx = _rows("x", x)
+    with _on(x, stream) as handle:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+        _, sy = _rows("out", y, x.shape)
+        mean, rstd = (torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+                      for _ in range(2))
+        if x.numel() == 0 and N > 0:
+            return y, mean, rstd
+        st = vidattn_layernorm(x, weight, bias, y, mean, rstd, B, H, S, N, sx, sy, x_type, p_type,
+                               eps, handle)
+    if st != VIDATTN_OK:
+        raise RuntimeError(f"vidattn_layernorm failed: {status_string(st)} ({st})")
+    return y, mean, rstd
+
+
+def layer_norm_bwd(dy, x, mean, rstd, weight=None, out=None, stream=None, params=True):
+    """The gradients of ``layer_norm``: (dx, dweight, dbias), the last two None
+    without a weight or with ``params=False`` (then only dx is computed).  dy: as y, any
+    strides; x, weight: as given to it; mean, rstd: as it returned them; dx is
+    contiguous, or ``out`` (which may be dy or x); raises on error."""
+    import torch
+    x_type, p_type = _check_norm(x, dict(dy=dy, out=out), weight, None)
+    (B, H, S, N), sx = _rows("x", x)
+    _, sdy = _rows("dy", dy, x.shape)
+    _check_tensors(dict(mean=mean, rstd=rstd), torch.float32)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t.shape != x.shape[:-1] or t.device != x.device:
+            raise ValueError(f"{name} must be {tuple(x.shape[:-1])} on {x.device} (is "
+                             f"{tuple(t.shape)} on {t.device})")
+    with _on(x, stream) as handle:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+        _, sdx = _rows("out", dx, x.shape)
+        dw = db = ws = None
+        n = 0
+        if weight is not None and params:
+            dw, db = torch.empty_like(weight), torch.empty_like(weight)
+            if x.numel() == 0:
+                return dx, dw.zero_(), db.zero_()
+            n = layernorm_bwd_workspace(B, H, S, N, x_type)
+            ws = torch.empty(max(n, 0), dtype=torch.uint8, device=x.device)
+        if x.numel() == 0 and N > 0:
+            return dx, None, None
+        st = vidattn_layernorm_bwd(dy, x, mean, rstd, weight, dx, dw, db, B, H, S, N, sdy, sx, sdx,
+                                   x_type, p_type, ws, n, handle)
+    if st != VIDATTN_OK:
+        raise RuntimeError(f"vidattn_layernorm_bwd failed: {status_string(st)} ({st})")
+    return dx, dw, db
+
+
 VIDATTN_ROPE_HALF_SPLIT = 1
 
 
@@ -374,6 +517,107 @@ def rope3d(q, k=None, grid=None, bands=None, theta=10000.0, interleaved=True, to
     if st != VIDATTN_OK:
         raise RuntimeError(f"vidattn_rope3d failed: {status_string(st)} ({st})")
     return out_q, out_k
+
+
+VIDATTN_ROPE_TRANSPOSE = 2
+
+
+def vidattn_rope3d_scaled(q_in, k_in, q_out, k_out, B, H, S, D, in_strides, out_strides, T, Hg, Wg,
+                          token_offset, d_t, d_h, d_w, freqs, pos_scale, amplitude, flags,
+                          stream=None) -> int:
+    """Enqueue the scaled 3D rotary embedding of q (and k) on ``stream``.
+    freqs, pos_scale: sequences of floats.  Returns the status."""
+    return load_library().vidattn_rope3d_scaled(
+        _ptr(q_in), _ptr(k_in), _ptr(q_out), _ptr(k_out), int(B), int(H), int(S), int(D),
+        _strides(in_strides), _strides(out_strides), int(T), int(Hg), int(Wg), int(token_offset),
+        int(d_t), int(d_h), int(d_w), (ctypes.c_double * max(len(freqs), 1))(*freqs),
+        (ctypes.c_double * 3)(*pos_scale), float(amplitude), int(flags), _stream(stream))
+
+
+def _rope_scaled(name, q, k, grid, bands, freqs, pos_scale, amplitude, interleaved, token_offset,
+                 out_q, out_k, stream, transpose):
+    import torch
+    _check_tensors(dict(q=q, k=k, out_q=out_q, out_k=out_k), torch.bfloat16, ndim=4,
+                   contiguous=False)
+    if out_k is not None and k is None:
+        raise ValueError("out_k without k")
+    (B, H, S, D), s_in = _rows("q", q)
+    if k is not None and _rows("k", k, q.shape)[1] != s_in:
+        raise ValueError("q and k must have the same strides")
+    if len(bands) != 3 or any(d < 0 or d % 2 for d in bands) or sum(bands) > D:
+        raise ValueError(f"bands must be 3 even sizes of at most {D} together (are {bands})")
+    if len(freqs) != sum(bands) // 2:
+        raise ValueError(f"freqs must hold {sum(bands) // 2} values, one a pair (holds "
+                         f"{len(freqs)})")
+    if len(pos_scale) != 3:
+        raise ValueError("pos_scale must hold 3 values")
+    with _on(q, stream) as handle:
+        if out_q is None:
+            out_q = torch.empty((B, H, S, D), dtype=q.dtype, device=q.device)
+        _, s_out = _rows("out_q", out_q, q.shape)
+        if k is not None:
+            if out_k is None:
+                out_k = torch.empty_strided(out_q.shape, out_q.stride(), dtype=k.dtype,
+                                            device=k.device)
+            if _rows("out_k", out_k, q.shape)[1] != s_out:
+                raise ValueError("out_q and out_k must have the same strides")
+        if q.numel() == 0 and D > 0:
+            return out_q, out_k
+        flags = (0 if interleaved else VIDATTN_ROPE_HALF_SPLIT) | \
+            (VIDATTN_ROPE_TRANSPOSE if transpose else 0)
+        st = vidattn_rope3d_scaled(q, k, out_q, out_k, B, H, S, D, s_in, s_out, *grid,
+                                   token_offset, *bands, freqs, pos_scale, amplitude, flags,
+                                   handle)
+    if st != VIDATTN_OK:
+        raise RuntimeError(f"{name} failed: {status_string(st)} ({st})")
+    return out_q, out_k
+
+
+def rope3d_scaled(q, k=None, grid=None, bands=None, freqs=None, pos_scale=(1.0, 1.0, 1.0),
+                  amplitude=1.0, interleaved=True, token_offset=0, out_q=None, out_k=None,
+                  stream=None):
+    """Rotate q (and k) with the caller's frequencies: pair c of the bands turns
+    by coord * pos_scale[axis] * freqs[c] and is scaled by amplitude; features
+    behind the bands and tokens outside the video are copied.  q, k: bf16
+    [B,H,S,D] of equal strides, the last dim contiguous; grid = (T, Hg, Wg);
+    bands = (d_t, d_h, d_w), at most D together; freqs: one float a pair (see
+    rope3d_frequencies).  Outputs are contiguous, or out_q and out_k of any
+    equal strides (out_q=q, out_k=k: in place).  Returns (q_rot, k_rot or None)."""
+    return _rope_scaled("vidattn_rope3d_scaled", q, k, grid, bands, freqs, pos_scale, amplitude,
+                        interleaved, token_offset, out_q, out_k, stream, False)
+
+
+def rope3d_scaled_bwd(dq, dk=None, grid=None, bands=None, freqs=None, pos_scale=(1.0, 1.0, 1.0),
+                      amplitude=1.0, interleaved=True, token_offset=0, out_q=None, out_k=None,
+                      stream=None):
+    """The gradients of rope3d_scaled's inputs from those of its outputs: the
+    transposed rotation, same arguments, same layouts."""
+    return _rope_scaled("vidattn_rope3d_scaled", dq, dk, grid, bands, freqs, pos_scale, amplitude,
+                        interleaved, token_offset, out_q, out_k, stream, True)
+
+
+def rope3d_frequencies(bands, theta=10000.0, extent=None, factor=1.0, turns=(1.0, 8.0)):
+    """Frequencies for rope3d_scaled: theta^(-2c/d) for pair c of a band of d
+    features, as vidattn_rope3d's.  With ``extent`` = the trained volume
+    (T, Hg, Wg), stretched by parts for one ``factor`` times as long on every
+    axis: a pair that turns fewer than turns[0] times over the trained extent
+    is interpolated (its frequency divided by factor), one that turns more than
+    turns[1] times is kept, linear in between."""
+    import math
+    if len(bands) != 3 or any(d < 0 or d % 2 for d in bands):
+        raise ValueError(f"bands must be 3 even sizes (are {bands})")
+    if not (theta > 0 and factor > 0 and turns[1] > turns[0]):
+        raise ValueError("theta and factor must be positive, turns ascending")
+    out = []
+    for a, d in enumerate(bands):
+        for c in range(d // 2):
+            w = theta ** (-2.0 * c / d)
+            if extent is not None:
+                n = extent[a] * w / (2 * math.pi)
+                keep = min(1.0, max(0.0, (n - turns[0]) / (turns[1] - turns[0])))
+                w = w * keep + w / factor * (1.0 - keep)
+            out.append(w)
+    return out
 
 
 VIDATTN_WINDOW_CLAMPED = 1

@@ -3,7 +3,9 @@
 #pragma once
 #include <cuda.h>
 
+#include <algorithm>
 #include <cstdint>
+#include <utility>
 
 namespace vidattn {
 namespace host {
@@ -22,6 +24,21 @@ int epoch();
 
 inline bool aligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+// Do the rows (N neighbouring elements each) of a [B,H,S,N] array with these
+// sizes and strides of its first three axes lie apart?
+inline bool rows_apart(const int64_t sizes[3], const int64_t strides[3], int64_t N) {
+  std::pair<int64_t, int64_t> d[3];
+  for (int i = 0; i < 3; ++i) d[i] = {strides[i], sizes[i]};
+  std::sort(d, d + 3);
+  int64_t end = N;   // one past the last element of what is laid out so far
+  for (const auto& x : d) {
+    if (x.second <= 1) continue;
+    if (x.first < end) return false;
+    end += x.first * (x.second - 1);
+  }
+  return true;
 }
 
 }  // namespace host

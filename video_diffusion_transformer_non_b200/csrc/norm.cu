@@ -1,0 +1,229 @@
+// Host side of the layer norm (vidattn_layernorm, vidattn_layernorm_bwd):
+// argument checks and the choice of kernel.  The operations are documented in
+// include/vidattn.h, the kernels in layernorm.cuh.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <map>
+#include <mutex>
+#include <utility>
+
+#include "../../include/vidattn.h"
+#include "internal.h"
+#include "layernorm.cuh"
+
+namespace vidattn {
+namespace {
+
+using LnKernel = void (*)(const LnParams);
+
+struct LnChoice {
+  LnKernel kernel;
+  int threads, rows;   // threads a CTA; rows a CTA takes at a time
+};
+
+template <typename X, int kLanes, int kC, int kR, bool kVec, int kMaxThreads>
+LnKernel ln_kernel(bool bwd) {
+  return bwd ? ln_bwd_kernel<X, kLanes, kC, kR, kVec, kMaxThreads>
+             : ln_fwd_kernel<X, kLanes, kC, kR, kVec, kMaxThreads>;
+}
+
+// The smallest form that holds a row of N features in registers.
+template <typename X, bool kVec>
+LnChoice ln_choose_x(bool bwd, int N) {
+  auto part = [&](LnKernel k, int lanes, int r) {
+    return LnChoice{k, kLnThreads, kLnThreads / lanes * r};
+  };
+  if (N <= 64) return part(ln_kernel<X, 8, 1, 4, kVec, kLnThreads>(bwd), 8, 4);
+  if (N <= 128) return part(ln_kernel<X, 16, 1, 4, kVec, kLnThreads>(bwd), 16, 4);
+  if (N <= 256) return part(ln_kernel<X, 32, 1, 4, kVec, kLnThreads>(bwd), 32, 4);
+  if (N <= 512) return part(ln_kernel<X, 32, 2, 2, kVec, kLnThreads>(bwd), 32, 2);
+  if (N <= 1024) return part(ln_kernel<X, 32, 4, 1, kVec, kLnThreads>(bwd), 32, 1);
+  const int threads = (N + 255) / 256 * 32;
+  if (threads <= 640) return LnChoice{ln_kernel<X, 0, 1, 2, kVec, 640>(bwd), threads, 2};
+  if (threads <= 1024) return LnChoice{ln_kernel<X, 0, 1, 1, kVec, 1024>(bwd), threads, 1};
+  return LnChoice{ln_kernel<X, 0, 2, 1, kVec, 1024>(bwd), (N + 511) / 512 * 32, 1};
+}
+LnChoice ln_choose(bool bwd, bool bf16, bool vec, int N) {
+  if (bf16) return vec ? ln_choose_x<uint16_t, true>(bwd, N) : ln_choose_x<uint16_t, false>(bwd, N);
+  return vec ? ln_choose_x<float, true>(bwd, N) : ln_choose_x<float, false>(bwd, N);
+}
+
+// CTAs of a launch: enough for all rows, at most what the device holds at once
+// (every CTA then walks over rows and reads the parameters once).
+std::mutex g_ln_mu;
+std::map<std::pair<int, std::pair<LnKernel, int>>, int> g_ln_resident;
+int ln_grid(int dev, int sms, const LnChoice& c, int64_t rows) {
+  int per_sm = 0;
+  {
+    std::lock_guard<std::mutex> lk(g_ln_mu);
+    int& known = g_ln_resident[{dev, {c.kernel, c.threads}}];
+    if (known == 0 && cudaOccupancyMaxActiveBlocksPerMultiprocessor(&known, c.kernel, c.threads,
+                                                                    0) != cudaSuccess)
+      known = 0;
+    per_sm = known;
+  }
+  if (per_sm < 1) return 0;
+  return int(std::min<int64_t>((rows + c.rows - 1) / c.rows, int64_t(sms) * per_sm));
+}
+// The most CTAs a backward launch of these sizes uses on any device it runs
+// on (sm_100a: at most 148 SMs x 2048 threads).
+int64_t ln_bwd_parts(const LnChoice& c, int64_t rows) {
+  return std::min<int64_t>((rows + c.rows - 1) / c.rows, 148 * (2048 / c.threads));
+}
+
+bool ln_apart(int B, int H, int S, int N, const int64_t s[3]) {
+  const int64_t sizes[3] = {B, H, S};
+  return host::rows_apart(sizes, s, N);
+}
+// Any read layout: strides not negative.
+bool ln_readable(const int64_t s[3]) { return s[0] >= 0 && s[1] >= 0 && s[2] >= 0; }
+bool ln_vector(const void* p, const int64_t s[3], int item) {
+  return host::aligned(p, 16) && s[0] * item % 16 == 0 && s[1] * item % 16 == 0 &&
+         s[2] * item % 16 == 0;
+}
+LnLayout ln_layout(const int64_t s[3]) { return LnLayout{s[0], s[1], s[2]}; }
+
+bool ln_sizes_ok(int B, int H, int S, int N) {
+  return B >= 1 && H >= 1 && S >= 0 && N >= 1 && N <= kLnMaxN &&
+         int64_t(B) * H <= INT_MAX && int64_t(B) * H * S <= INT_MAX;
+}
+bool ln_type_ok(int t) { return t == VIDATTN_BF16 || t == VIDATTN_F32; }
+int ln_item(int t) { return t == VIDATTN_BF16 ? 2 : 4; }
+
+}  // namespace
+}  // namespace vidattn
+
+using namespace vidattn;
+
+extern "C" {
+
+VIDATTN_API int vidattn_layernorm(const void* x, const void* weight, const void* bias, void* y,
+                                  float* mean, float* rstd, int B, int H, int S, int N,
+                                  const int64_t* x_strides, const int64_t* y_strides, int x_type,
+                                  int param_type, double eps, vidattn_stream_t stream_) {
+  if (!x_strides || !y_strides) return VIDATTN_ERR_NULL;
+  if (!ln_sizes_ok(B, H, S, N) || !ln_type_ok(x_type) || !ln_type_ok(param_type) ||
+      !std::isfinite(eps) || eps < 0.0 || !ln_readable(x_strides) ||
+      !ln_apart(B, H, S, N, y_strides))
+    return VIDATTN_ERR_BAD_SHAPE;
+  if (S == 0) return VIDATTN_OK;
+  if (!x || !y) return VIDATTN_ERR_NULL;
+  const int item = ln_item(x_type), pitem = ln_item(param_type);
+  if (!host::aligned(x, item) || !host::aligned(y, item) || !host::aligned(weight, pitem) ||
+      !host::aligned(bias, pitem) || !host::aligned(mean, 4) || !host::aligned(rstd, 4))
+    return VIDATTN_ERR_MISALIGNED;
+  int dev = 0, sms = 0;
+  int* err = nullptr;
+  const int st = host::device(&dev, &err, &sms);
+  if (st != VIDATTN_OK) return st;
+  LnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.x = x;
+  p.w = weight;
+  p.b = bias;
+  p.y = y;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.lx = ln_layout(x_strides);
+  p.ly = ln_layout(y_strides);
+  p.rows = B * H * S;
+  p.N = N;
+  p.div_s = make_fastdiv(uint32_t(S));
+  p.div_h = make_fastdiv(uint32_t(H));
+  p.params_bf16 = param_type == VIDATTN_BF16;
+  p.eps = float(eps);
+  const bool vec = N % 8 == 0 && ln_vector(x, x_strides, item) && ln_vector(y, y_strides, item);
+  const LnChoice c = ln_choose(false, x_type == VIDATTN_BF16, vec, N);
+  const int grid = ln_grid(dev, sms, c, p.rows);
+  if (grid < 1) return VIDATTN_ERR_CUDA;
+  c.kernel<<<grid, c.threads, 0, reinterpret_cast<cudaStream_t>(stream_)>>>(p);
+  return cudaGetLastError() == cudaSuccess ? VIDATTN_OK : VIDATTN_ERR_CUDA;
+}
+
+VIDATTN_API int64_t vidattn_layernorm_bwd_workspace(int B, int H, int S, int N, int x_type) {
+  if (!ln_sizes_ok(B, H, S, N) || !ln_type_ok(x_type)) return -1;
+  const LnChoice c = ln_choose(true, x_type == VIDATTN_BF16, true, N);
+  return (ln_bwd_parts(c, int64_t(B) * H * S) * 2 * N * 4 + 255) & ~int64_t(255);
+}
+
+VIDATTN_API int vidattn_layernorm_bwd(const void* dy, const void* x, const float* mean,
+                                      const float* rstd, const void* weight, void* dx,
+                                      void* dweight, void* dbias, int B, int H, int S, int N,
+                                      const int64_t* dy_strides, const int64_t* x_strides,
+                                      const int64_t* dx_strides, int x_type, int param_type,
+                                      void* workspace, int64_t workspace_bytes,
+                                      vidattn_stream_t stream_) {
+  if (!dy_strides || !x_strides || !dx_strides) return VIDATTN_ERR_NULL;
+  if (!ln_sizes_ok(B, H, S, N) || !ln_type_ok(x_type) || !ln_type_ok(param_type) ||
+      !ln_readable(x_strides) || !ln_readable(dy_strides) ||
+      !ln_apart(B, H, S, N, dx_strides))
+    return VIDATTN_ERR_BAD_SHAPE;
+  const int item = ln_item(x_type), pitem = ln_item(param_type);
+  const bool params = dweight || dbias;
+  if (S > 0 && (!dy || !x || !mean || !rstd || !dx || (params && !workspace)))
+    return VIDATTN_ERR_NULL;
+  if (!host::aligned(x, item) || !host::aligned(dy, item) || !host::aligned(dx, item) ||
+      !host::aligned(weight, pitem) || !host::aligned(dweight, pitem) ||
+      !host::aligned(dbias, pitem) || !host::aligned(mean, 4) || !host::aligned(rstd, 4) ||
+      (params && !host::aligned(workspace, 256)))
+    return VIDATTN_ERR_MISALIGNED;
+  if (S > 0 && params &&
+      workspace_bytes < vidattn_layernorm_bwd_workspace(B, H, S, N, x_type))
+    return VIDATTN_ERR_SCRATCH_LIMIT;
+  if (S == 0 && !params) return VIDATTN_OK;
+  int dev = 0, sms = 0;
+  int* err = nullptr;
+  const int st = host::device(&dev, &err, &sms);
+  if (st != VIDATTN_OK) return st;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (S == 0) {   // sums over no rows
+    bool ok = true;
+    for (void* d : {dweight, dbias})
+      if (d) ok = ok && cudaMemsetAsync(d, 0, size_t(N) * pitem, stream) == cudaSuccess;
+    return ok ? VIDATTN_OK : VIDATTN_ERR_CUDA;
+  }
+  LnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.x = x;
+  p.dy = dy;
+  p.w = weight;
+  p.y = dx;
+  p.mean = const_cast<float*>(mean);
+  p.rstd = const_cast<float*>(rstd);
+  p.part = params ? static_cast<float*>(workspace) : nullptr;
+  p.lx = ln_layout(x_strides);
+  p.ldy = ln_layout(dy_strides);
+  p.ly = ln_layout(dx_strides);
+  p.rows = B * H * S;
+  p.N = N;
+  p.div_s = make_fastdiv(uint32_t(S));
+  p.div_h = make_fastdiv(uint32_t(H));
+  p.params_bf16 = param_type == VIDATTN_BF16;
+  const bool vec = N % 8 == 0 && ln_vector(x, x_strides, item) && ln_vector(dy, dy_strides, item) &&
+                   ln_vector(dx, dx_strides, item);
+  const LnChoice c = ln_choose(true, x_type == VIDATTN_BF16, vec, N);
+  int grid = ln_grid(dev, sms, c, p.rows);
+  if (grid < 1) return VIDATTN_ERR_CUDA;
+  grid = int(std::min<int64_t>(grid, ln_bwd_parts(c, p.rows)));
+  c.kernel<<<grid, c.threads, 0, stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return VIDATTN_ERR_CUDA;
+  if (params) {
+    const unsigned blocks = (2 * N + 31) / 32;
+    if (p.params_bf16)
+      ln_params_grad_kernel<<<blocks, 1024, 0, stream>>>(
+          p.part, grid, N, static_cast<uint16_t*>(dweight), static_cast<uint16_t*>(dbias));
+    else
+      ln_params_grad_kernel<<<blocks, 1024, 0, stream>>>(
+          p.part, grid, N, static_cast<float*>(dweight), static_cast<float*>(dbias));
+    if (cudaGetLastError() != cudaSuccess) return VIDATTN_ERR_CUDA;
+  }
+  return VIDATTN_OK;
+}
+
+}  // extern "C"

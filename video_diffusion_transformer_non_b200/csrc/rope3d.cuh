@@ -19,6 +19,12 @@
 // interleaved pairing finds both features of a pair in one chunk; the
 // half-split pairing stages the chunk in shared memory and reads the partner
 // feature from the neighbouring thread of the same row.
+//
+// kScaled (vidattn_rope3d_scaled): frequencies and an amplitude of the
+// caller's, bands over a part of the head, output strides, and the transposed
+// rotation (the gradient).  What is not rotated keeps its bits there even next
+// to an infinity or a NaN, and when the token tiles are fewer than the CTAs
+// the device holds, gridDim.y CTAs share a tile's slabs.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -41,7 +47,12 @@ struct RopeParams {
   FastDiv div_bh, div_h;       // by B * H and by H
   int n_video, hw, Hg, Wg, offset;
   int col_h, col_w;            // first table column of the h band and of the w band
-  double freq[kRopeMaxD / 2];  // per table column: theta^(-2k/d)
+  // kScaled only: output strides, table columns in use (the pairs of the
+  // bands), and the amplitude, negative sine for the transposed rotation
+  long long osb, osh, oss;
+  int n_cols;
+  float cos_mul, sin_mul;
+  double freq[kRopeMaxD / 2];  // per table column: theta^(-2k/d), or the caller's
   // per feature e: its table column, its partner feature, and 1 when e is the
   // first feature of its pair (its partner's term enters with a minus sign)
   uint8_t col[kRopeMaxD], partner[kRopeMaxD], first[kRopeMaxD];
@@ -56,7 +67,7 @@ __device__ __forceinline__ void st_stream_v4(uint16_t* p, uint4 v) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-template <int D, bool kInterleaved>
+template <int D, bool kInterleaved, bool kScaled>
 __global__ void __launch_bounds__(kRopeThreads) rope3d_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kHalf = D / 2;
   constexpr int kChunks = D / 8;                           // 16-byte chunks per row
@@ -74,6 +85,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope3d_kernel(const __grid_const
   const int slab_lane = tid / kPerSlab;
   const int n_tiles = (p.S + kRopeTokens - 1) / kRopeTokens;
 
+  const int slab0 = kScaled ? blockIdx.y * kSlabsPerPass : 0;
+  const int slab_step = kSlabsPerPass * (kScaled ? gridDim.y : 1);
+
   // this thread's features: table columns, and for the half-split pairing
   // the partner's position in the staged row
   int col[8], partner_chunk[8], partner_elem[8];
@@ -86,6 +100,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope3d_kernel(const __grid_const
     partner_chunk[e] = p.partner[f] / 8;
     partner_elem[e] = p.partner[f] % 8;
   }
+  // kScaled: this thread's features inside the bands, as bits
+  uint32_t in_bands = 0;
+  if constexpr (kScaled) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) in_bands |= (ch * 8 + e < 2 * p.n_cols ? 1u : 0u) << e;
+  }
 
   int parity = 0;
   for (int tile = blockIdx.x; tile < n_tiles; tile += gridDim.x, parity ^= 1) {
@@ -97,12 +117,16 @@ __global__ void __launch_bounds__(kRopeThreads) rope3d_kernel(const __grid_const
       const int r = i / kHalf, c = i % kHalf;
       const int n = s0 + r - p.offset;
       float cv = 1.f, sv = 0.f;
-      if (n >= 0 && n < p.n_video) {
+      if (n >= 0 && n < p.n_video && (!kScaled || c < p.n_cols)) {
         const int coord = c < p.col_h ? n / p.hw : (c < p.col_w ? (n / p.Wg) % p.Hg : n % p.Wg);
         const double two_pi = 6.283185307179586476925286766559;
         double a = double(coord) * p.freq[c];
         a -= two_pi * rint(a / two_pi);
         sincosf(float(a), &sv, &cv);
+        if constexpr (kScaled) {
+          cv *= p.cos_mul;
+          sv *= p.sin_mul;
+        }
       }
       tb[r][c] = make_float2(cv, sv);
     }
@@ -129,13 +153,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope3d_kernel(const __grid_const
     }
     const int s = s0 + row;
     const bool row_ok = s < p.S;
+    const uint32_t turned = s >= p.offset && s - p.offset < p.n_video ? in_bands : 0u;
 
-    for (int base = slab_lane; base < p.n_slabs; base += kSlabsPerPass * kRopeUnroll) {
+    for (int base = slab0 + slab_lane; base < p.n_slabs; base += slab_step * kRopeUnroll) {
       uint4 v[kRopeUnroll];
       uint16_t* dst[kRopeUnroll];
 #pragma unroll
       for (int u = 0; u < kRopeUnroll; ++u) {
-        const int slab = base + u * kSlabsPerPass;
+        const int slab = base + u * slab_step;
         v[u] = make_uint4(0, 0, 0, 0);
         dst[u] = nullptr;
         if (row_ok && slab < p.n_slabs) {
@@ -144,7 +169,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope3d_kernel(const __grid_const
           const uint32_t b = fastdiv(bh, p.div_h);
           const uint32_t h = bh - b * p.div_h.d;
           const uint16_t* src = p.in[t] + b * p.sb + h * p.sh + s * p.ss + ch * 8;
-          dst[u] = p.out[t] + (static_cast<long long>(bh) * p.S + s) * D + ch * 8;
+          if constexpr (kScaled)
+            dst[u] = p.out[t] + b * p.osb + h * p.osh + s * p.oss + ch * 8;
+          else
+            dst[u] = p.out[t] + (static_cast<long long>(bh) * p.S + s) * D + ch * 8;
           v[u] = ld_stream_v4(src);
         }
       }
@@ -180,6 +208,15 @@ __global__ void __launch_bounds__(kRopeThreads) rope3d_kernel(const __grid_const
           o.y = pack_bf16x2(y[2], y[3]);
           o.z = pack_bf16x2(y[4], y[5]);
           o.w = pack_bf16x2(y[6], y[7]);
+          if constexpr (kScaled) {
+            if (turned != 0xffu) {   // bands end on a pair: words are turned or kept whole
+              const uint32_t ow[4] = {o.x, o.y, o.z, o.w};
+              uint32_t r[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) r[j] = (turned >> (2 * j)) & 1u ? ow[j] : w[j];
+              o = make_uint4(r[0], r[1], r[2], r[3]);
+            }
+          }
           st_stream_v4(dst[u], o);
         }
       }

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -93,7 +94,7 @@ struct DeviceInfo {
   bool ok = false;
   uint32_t attrs_set = 0;   // bit (kernel variant index) once its smem limit is raised
   int* err = nullptr;       // device address of g_device_error on this device
-  int rope_grid[4] = {};    // persistent grid of each rope3d variant (SMs x resident CTAs)
+  int rope_grid[8] = {};    // persistent grid of each rope3d variant (SMs x resident CTAs)
   int sms = 0;              // streaming multiprocessors (the attention kernel's grid bound)
   // vidattn_fwd_host's copy streams (host-to-device, device-to-host) and
   // its second compute stream
@@ -478,10 +479,14 @@ __global__ void selftest_timeout_kernel(int* err, unsigned long long timeout_ns)
 using RopeKernel = void (*)(const RopeParams);
 RopeKernel rope_variant(int i) {
   switch (i) {
-    case 0: return rope3d_kernel<64, true>;
-    case 1: return rope3d_kernel<64, false>;
-    case 2: return rope3d_kernel<128, true>;
-    default: return rope3d_kernel<128, false>;
+    case 0: return rope3d_kernel<64, true, false>;
+    case 1: return rope3d_kernel<64, false, false>;
+    case 2: return rope3d_kernel<128, true, false>;
+    case 3: return rope3d_kernel<128, false, false>;
+    case 4: return rope3d_kernel<64, true, true>;
+    case 5: return rope3d_kernel<64, false, true>;
+    case 6: return rope3d_kernel<128, true, true>;
+    default: return rope3d_kernel<128, false, true>;
   }
 }
 
@@ -500,14 +505,16 @@ int rope_grid(int dev, int i) {
   return info.rope_grid[i];
 }
 
-// Fills the per-column frequencies and the per-feature pairing tables.
-void rope_tables(RopeParams& p, int D, const int bands[3], double theta, bool half_split) {
+// Fills the per-feature pairing tables and, from theta, the per-column
+// frequencies (freqs null), or takes the given ones times the axis' scale.
+void rope_tables(RopeParams& p, const int bands[3], double theta, bool half_split,
+                 const double* freqs = nullptr, const double* pos_scale = nullptr) {
   int start = 0;
   for (int a = 0; a < 3; ++a) {
     const int d = bands[a], half = d / 2;
     for (int k = 0; k < half; ++k) {
       const int c = start / 2 + k;
-      p.freq[c] = std::pow(theta, -2.0 * k / d);
+      p.freq[c] = freqs ? freqs[c] * pos_scale[a] : std::pow(theta, -2.0 * k / d);
       const int f0 = half_split ? start + k : start + 2 * k;
       const int f1 = half_split ? start + k + half : start + 2 * k + 1;
       p.col[f0] = p.col[f1] = static_cast<uint8_t>(c);
@@ -518,7 +525,43 @@ void rope_tables(RopeParams& p, int D, const int bands[3], double theta, bool ha
     }
     start += d;
   }
-  (void)D;
+}
+
+// The checks that both rotary entry points share (bands: even, none negative).
+int rope_check(const void* q_in, const void* k_in, const void* q_out, const void* k_out, int B,
+               int H, int S, int D, int T, int Hg, int Wg, int token_offset, const int bands[3],
+               int n_tensors) {
+  if (B < 1 || H < 1 || S < 1 || int64_t(n_tensors) * B * H >= (int64_t(1) << 31))
+    return VIDATTN_ERR_BAD_SHAPE;
+  if (T < 1 || Hg < 1 || Wg < 1 || token_offset < 0 ||
+      int64_t(T) * Hg > S || int64_t(token_offset) + int64_t(T) * Hg * Wg > S)
+    return VIDATTN_ERR_BAD_SHAPE;
+  for (int a = 0; a < 3; ++a)
+    if (bands[a] < 0 || bands[a] > D || bands[a] % 2) return VIDATTN_ERR_BAD_SHAPE;
+  for (const void* p : {q_in, k_in, q_out, k_out})
+    if (p && !aligned(p, 16)) return VIDATTN_ERR_MISALIGNED;
+  return VIDATTN_OK;
+}
+
+// The fields that both rotary entry points set the same way.
+void rope_common(RopeParams& p, const void* q_in, const void* k_in, void* q_out, void* k_out, int B,
+                 int H, int S, int T, int Hg, int Wg, int token_offset, const int bands[3],
+                 int n_tensors) {
+  p.in[0] = static_cast<const uint16_t*>(q_in);
+  p.out[0] = static_cast<uint16_t*>(q_out);
+  p.in[1] = static_cast<const uint16_t*>(k_in ? k_in : q_in);
+  p.out[1] = static_cast<uint16_t*>(k_out ? k_out : q_out);
+  p.n_slabs = n_tensors * B * H;
+  p.S = S;
+  p.div_bh = make_fastdiv(uint32_t(B) * uint32_t(H));
+  p.div_h = make_fastdiv(uint32_t(H));
+  p.n_video = T * Hg * Wg;
+  p.hw = Hg * Wg;
+  p.Hg = Hg;
+  p.Wg = Wg;
+  p.offset = token_offset;
+  p.col_h = bands[0] / 2;
+  p.col_w = (bands[0] + bands[1]) / 2;
 }
 
 }  // namespace
@@ -900,51 +943,99 @@ VIDATTN_API int vidattn_rope3d(const void* q_in, const void* k_in, void* q_out, 
   if (D != 64 && D != 128) return VIDATTN_ERR_UNSUPPORTED_D;
   if (flags & ~VIDATTN_ROPE_HALF_SPLIT) return VIDATTN_ERR_BAD_SHAPE;
   const int n_tensors = k_in ? 2 : 1;
-  if (B < 1 || H < 1 || S < 1 || int64_t(n_tensors) * B * H >= (int64_t(1) << 31))
-    return VIDATTN_ERR_BAD_SHAPE;
-  if (T < 1 || Hg < 1 || Wg < 1 || token_offset < 0 ||
-      int64_t(token_offset) + int64_t(T) * Hg * Wg > S)
-    return VIDATTN_ERR_BAD_SHAPE;
   const int bands[3] = {d_t, d_h, d_w};
-  for (int a = 0; a < 3; ++a)
-    if (bands[a] < 0 || bands[a] % 2) return VIDATTN_ERR_BAD_SHAPE;
+  int st = rope_check(q_in, k_in, q_out, k_out, B, H, S, D, T, Hg, Wg, token_offset, bands,
+                      n_tensors);
+  if (st == VIDATTN_ERR_BAD_SHAPE) return st;
   if (d_t + d_h + d_w != D) return VIDATTN_ERR_BAD_SHAPE;
   if (!std::isfinite(theta) || !(theta > 0.0)) return VIDATTN_ERR_BAD_SHAPE;
-  if (!aligned(q_in, 16) || !aligned(q_out, 16) || (k_in && (!aligned(k_in, 16) || !aligned(k_out, 16))))
-    return VIDATTN_ERR_MISALIGNED;
+  if (st != VIDATTN_OK) return st;
   if (stride_b % 8 || stride_h % 8 || stride_s % 8) return VIDATTN_ERR_MISALIGNED;
   int dev = 0;
-  int st = ensure_device(&dev);
+  st = ensure_device(&dev);
   if (st != VIDATTN_OK) return st;
 
   const bool half_split = (flags & VIDATTN_ROPE_HALF_SPLIT) != 0;
   RopeParams p;
   std::memset(&p, 0, sizeof(p));
-  p.in[0] = static_cast<const uint16_t*>(q_in);
-  p.out[0] = static_cast<uint16_t*>(q_out);
-  p.in[1] = static_cast<const uint16_t*>(k_in ? k_in : q_in);
-  p.out[1] = static_cast<uint16_t*>(k_out ? k_out : q_out);
+  rope_common(p, q_in, k_in, q_out, k_out, B, H, S, T, Hg, Wg, token_offset, bands, n_tensors);
   p.sb = stride_b;
   p.sh = stride_h;
   p.ss = stride_s;
-  p.n_slabs = n_tensors * B * H;
-  p.S = S;
-  p.div_bh = make_fastdiv(uint32_t(B) * uint32_t(H));
-  p.div_h = make_fastdiv(uint32_t(H));
-  p.n_video = T * Hg * Wg;
-  p.hw = Hg * Wg;
-  p.Hg = Hg;
-  p.Wg = Wg;
-  p.offset = token_offset;
-  p.col_h = d_t / 2;
-  p.col_w = (d_t + d_h) / 2;
-  rope_tables(p, D, bands, theta, half_split);
+  rope_tables(p, bands, theta, half_split);
 
   const int variant = (D == 128 ? 2 : 0) + (half_split ? 1 : 0);
   const int grid_max = rope_grid(dev, variant);
   if (grid_max <= 0) return VIDATTN_ERR_CUDA;
   const int n_tiles = (S + kRopeTokens - 1) / kRopeTokens;
   const int grid = n_tiles < grid_max ? n_tiles : grid_max;
+  rope_variant(variant)<<<grid, kRopeThreads, 0, reinterpret_cast<cudaStream_t>(stream_)>>>(p);
+  return cudaGetLastError() == cudaSuccess ? VIDATTN_OK : VIDATTN_ERR_CUDA;
+}
+
+VIDATTN_API int vidattn_rope3d_scaled(const void* q_in, const void* k_in, void* q_out,
+                                      void* k_out, int B, int H, int S, int D,
+                                      const int64_t* in_strides, const int64_t* out_strides,
+                                      int T, int Hg, int Wg, int token_offset, int d_t, int d_h,
+                                      int d_w, const double* freqs, const double* pos_scale,
+                                      double amplitude, int flags, vidattn_stream_t stream_) {
+  if (!q_in || !q_out || (k_in == nullptr) != (k_out == nullptr) || !in_strides || !out_strides ||
+      !freqs || !pos_scale)
+    return VIDATTN_ERR_NULL;
+  if (D != 64 && D != 128) return VIDATTN_ERR_UNSUPPORTED_D;
+  if (flags & ~(VIDATTN_ROPE_HALF_SPLIT | VIDATTN_ROPE_TRANSPOSE)) return VIDATTN_ERR_BAD_SHAPE;
+  const int n_tensors = k_in ? 2 : 1;
+  const int bands[3] = {d_t, d_h, d_w};
+  int st = rope_check(q_in, k_in, q_out, k_out, B, H, S, D, T, Hg, Wg, token_offset, bands,
+                      n_tensors);
+  if (st != VIDATTN_OK) return st;
+  const int n_cols = (d_t + d_h + d_w) / 2;
+  if (2 * n_cols > D || !std::isfinite(amplitude) || !std::isfinite(float(amplitude)))
+    return VIDATTN_ERR_BAD_SHAPE;
+  // fp64 holds an angle below 2^30 to 2^-23, half a step of the fp32 angle
+  // that it is reduced to
+  const double most = 1073741824.0;
+  for (int a = 0, c = 0; a < 3; ++a) {
+    const double far = (a == 0 ? T : a == 1 ? Hg : Wg) - 1;
+    for (int k = 0; k < bands[a] / 2; ++k, ++c) {
+      const double w = freqs[c] * pos_scale[a];
+      if (!std::isfinite(w) || std::fabs(w) * (far + 1) > most) return VIDATTN_ERR_BAD_SHAPE;
+    }
+  }
+  const int64_t sizes[3] = {B, H, S};
+  for (int i = 0; i < 3; ++i) {
+    if (in_strides[i] < 0) return VIDATTN_ERR_BAD_SHAPE;
+    if (in_strides[i] % 8 || out_strides[i] % 8) return VIDATTN_ERR_MISALIGNED;
+  }
+  if (!host::rows_apart(sizes, out_strides, D)) return VIDATTN_ERR_BAD_SHAPE;
+  int dev = 0;
+  st = ensure_device(&dev);
+  if (st != VIDATTN_OK) return st;
+
+  const bool half_split = (flags & VIDATTN_ROPE_HALF_SPLIT) != 0;
+  RopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  rope_common(p, q_in, k_in, q_out, k_out, B, H, S, T, Hg, Wg, token_offset, bands, n_tensors);
+  p.sb = in_strides[0];
+  p.sh = in_strides[1];
+  p.ss = in_strides[2];
+  p.osb = out_strides[0];
+  p.osh = out_strides[1];
+  p.oss = out_strides[2];
+  p.n_cols = n_cols;
+  p.cos_mul = float(amplitude);
+  p.sin_mul = (flags & VIDATTN_ROPE_TRANSPOSE) ? -p.cos_mul : p.cos_mul;
+  for (int f = 0; f < D; ++f) p.partner[f] = uint8_t(f);   // behind the bands: itself
+  rope_tables(p, bands, 0.0, half_split, freqs, pos_scale);
+
+  const int variant = 4 + (D == 128 ? 2 : 0) + (half_split ? 1 : 0);
+  const int grid_max = rope_grid(dev, variant);
+  if (grid_max <= 0) return VIDATTN_ERR_CUDA;
+  const int n_tiles = (S + kRopeTokens - 1) / kRopeTokens;
+  const int per_pass = kRopeThreads / (kRopeTokens * (D / 8));   // slabs a CTA takes at once
+  const int passes = (p.n_slabs + per_pass - 1) / per_pass;
+  dim3 grid(n_tiles < grid_max ? n_tiles : grid_max, 1);
+  grid.y = std::min(std::max(grid_max / int(grid.x), 1), std::min(passes, 65535));
   rope_variant(variant)<<<grid, kRopeThreads, 0, reinterpret_cast<cudaStream_t>(stream_)>>>(p);
   return cudaGetLastError() == cudaSuccess ? VIDATTN_OK : VIDATTN_ERR_CUDA;
 }
