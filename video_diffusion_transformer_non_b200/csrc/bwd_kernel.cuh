@@ -32,8 +32,7 @@
 namespace vidattn {
 
 constexpr int kBwdThreads = 384;
-constexpr int kBwdMaxListed = 4096;   // visited tiles listed in shared memory (with ids)
-constexpr int kBwdMaskBit = 1 << 15;
+constexpr int kBwdMaxListed = 3072;   // tiles of a unit's range whose visits are kept as bits
 
 struct BwdParams {
   // per 128-row query tile: -lse * log2(e) (row sees nothing or is past S_q:
@@ -65,23 +64,28 @@ struct BwdCfg {
   static constexpr int kSub = D / 64;
   static constexpr int kSubBytes = 128 * 128;
   static constexpr int kTileBytes = kSub * kSubBytes;
-  static constexpr int kStages = 2;
-  // two stationary tiles, then kStages pairs of moving tiles
+  // Two stationary tiles and two rings of moving tiles.  A tile of ring A is
+  // held from its score product to its gradient product, over more than a
+  // whole step, so that ring has one stage more (with 2 a load had to land
+  // between two products: 3500 cycles a step instead of 2100).  At D = 128
+  // the seven tiles leave 3 KB for everything else.
+  static constexpr int kStagesA = 3, kStagesB = 2;
   static constexpr int kOffFixed = 0;
   static constexpr int kOffRingA = 2 * kTileBytes;
-  static constexpr int kOffRingB = kOffRingA + kStages * kTileBytes;
-  static constexpr int kOffStats = kOffRingB + kStages * kTileBytes;   // [kStages][2][128] fp32
+  static constexpr int kOffRingB = kOffRingA + kStagesA * kTileBytes;
+  static constexpr int kOffStats = kOffRingB + kStagesB * kTileBytes;   // [kStagesB][2][128] fp32
   static constexpr int kStatBytes = 2 * 128 * 4;
-  static constexpr int kOffBar = kOffStats + kStages * kStatBytes;
-  // fixed_full[2] a_full[S] a_empty[S] b_full[S] b_empty[S] s_full s_free
-  // p_full dp_full ds_full ds_free[2] done
-  static constexpr int kNumBars = 2 + 4 * kStages + 8;
-  static constexpr int kOffMisc = kOffBar + 8 * kNumBars;   // tmem addr, abort flag, counts
-  static constexpr int kOffList = (kOffMisc + 16 + 13 * 4 + 127) & ~127;
-  static constexpr int kSmemBytes = kOffList + 2 * kBwdMaxListed + 1024;   // + alignment slack
+  static constexpr int kOffBar = kOffStats + kStagesB * kStatBytes;
+  // fixed_full[2] a_full[] a_empty[] b_full[] b_empty[] s_full s_free
+  // dp_full dp_free p_full ds_full ds_free[2] done
+  static constexpr int kNumBars = 2 + 2 * (kStagesA + kStagesB) + 9;
+  static constexpr int kOffMisc = kOffBar + 8 * kNumBars;   // tmem addr, abort flag
+  static constexpr int kOffList = kOffMisc + 16;            // visited tiles, masked tiles: bits
+  static constexpr int kSmemBytes = kOffList + 2 * kBwdMaxListed / 8;
   static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory on sm_100");
   static constexpr uint32_t kTmemCols = 512;
-  // KV units: dV [0,D), dK [128,128+D), S/P [256,384), dP/dS [384,512).
+  // KV units: dV [0,D), dK [128,128+D), S [256,384), dP [384,512), and over
+  // the dP columns [64h, 64h + 64) of half h, once read, P and dS (32 each).
   // Q units: dQ [0,D), dS buffers [128,192) and [192,256), S [256,384), dP [384,512).
   static constexpr uint32_t kTmemAcc0 = 0, kTmemAcc1 = 128, kTmemDS = 128, kTmemS = 256,
                             kTmemDP = 384;
@@ -127,11 +131,21 @@ __device__ __forceinline__ void bulk_load_elect(uint32_t dst, const void* src, u
       : "memory");
 }
 
-// The other-side tiles a unit walks: positions [t0, t1) of its visit sequence
-// (first + each list entry, or first, first + 1, ...).
+// The other-side tiles a unit walks: positions [t0, t1) of its visit sequence,
+// first + each set bit in turn (with ids), or first, first + 1, ...
 struct BwdWalk {
-  const uint16_t* list;
-  int first, t0, t1;
+  const uint32_t* bits;   // [kBwdMaxListed / 32] visited, then as many: needs the mask
+  int first, n, start;    // n tiles from position `start` (relative to first)
+  __device__ __forceinline__ int next(int pos) const {   // first visited position >= pos
+    if (bits == nullptr) return pos;
+    int w = pos >> 5;
+    uint32_t x = bits[w] & (~0u << (pos & 31));
+    while (x == 0u) x = bits[++w];
+    return (w << 5) + __ffs(x) - 1;
+  }
+  __device__ __forceinline__ bool masked(int pos) const {
+    return (bits[kBwdMaxListed / 32 + (pos >> 5)] >> (pos & 31)) & 1u;
+  }
 };
 
 // Is any pair of (query tile i, key tile j) hidden?  kv_side: the unit owns
@@ -173,13 +187,15 @@ __device__ __forceinline__ uint64_t bwd_mask64(int x0, int lo, int hi, const int
 // every 16, the last kEmu on the FMA pipe.
 template <int kEmu, bool kPerColumn>
 __device__ __forceinline__ void bwd_probs(uint32_t taddr, float c, float off, const float* offs,
-                                          float (&pr)[64]) {
+                                          uint32_t free_bar, float (&pr)[64]) {
   uint32_t r[2][32];
   tmem_ld32(taddr, r[0]);
   tmem_ld32(taddr + 32, r[1]);
   tmem_ld_wait();
   reg_fence(r[0]);
   reg_fence(r[1]);
+  tc_fence_before();
+  mbar_arrive(free_bar);   // the scores are in registers
   const float2 c2 = make_float2(c, c);
 #pragma unroll
   for (int x = 0; x < 64; x += 4) {
@@ -204,28 +220,21 @@ __device__ __forceinline__ void bwd_probs(uint32_t taddr, float c, float off, co
   }
 }
 
-// dS = P (dP - delta) of the same 64 columns, packed to bf16 pairs.
+// dS = P (dP - delta) of 32 columns (r: dP), packed to bf16 pairs.
 template <bool kPerColumn>
-__device__ __forceinline__ void bwd_dscores(uint32_t taddr, float nd, const float* nds,
-                                            const float (&pr)[64], uint32_t (&pk)[32]) {
-  uint32_t r[2][32];
-  tmem_ld32(taddr, r[0]);
-  tmem_ld32(taddr + 32, r[1]);
-  tmem_ld_wait();
-  reg_fence(r[0]);
-  reg_fence(r[1]);
+__device__ __forceinline__ void bwd_dscores32(const uint32_t (&r)[32], float nd, const float* nds,
+                                              const float* pr, uint32_t (&pk)[16]) {
 #pragma unroll
-  for (int x = 0; x < 64; x += 4) {
+  for (int x = 0; x < 32; x += 4) {
     float4 o = make_float4(nd, nd, nd, nd);
     if (kPerColumn) o = *reinterpret_cast<const float4*>(nds + x);
-    const float oo[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
     for (int y = 0; y < 4; y += 2) {
       const int e = x + y;
-      const float2 t = fadd2(make_float2(__uint_as_float(r[e >> 5][e & 31]),
-                                         __uint_as_float(r[e >> 5][(e & 31) + 1])),
-                             make_float2(oo[y], oo[y + 1]));
-      pk[e >> 1] = pack_bf16x2(pr[e] * t.x, pr[e + 1] * t.y);
+      const float2 t = fadd2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
+                             y == 0 ? make_float2(o.x, o.y) : make_float2(o.z, o.w));
+      const float2 ds = fmul2(make_float2(pr[e], pr[e + 1]), t);
+      pk[e >> 1] = pack_bf16x2(ds.x, ds.y);
     }
   }
 }
@@ -279,21 +288,26 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   auto bar = [&](int i) { return sbase + C::kOffBar + 8 * i; };
   auto fixed_full = [&](int i) { return bar(i); };
-  auto a_full = [&](int s) { return bar(2 + s); };
-  auto a_empty = [&](int s) { return bar(2 + C::kStages + s); };
-  auto b_full = [&](int s) { return bar(2 + 2 * C::kStages + s); };
-  auto b_empty = [&](int s) { return bar(2 + 3 * C::kStages + s); };
-  constexpr int kB0 = 2 + 4 * C::kStages;
-  const uint32_t s_full = bar(kB0), s_free = bar(kB0 + 1), p_full = bar(kB0 + 2),
-                 dp_full = bar(kB0 + 3), ds_full = bar(kB0 + 4), done = bar(kB0 + 7);
-  auto ds_free = [&](int i) { return bar(kB0 + 5 + i); };
+  constexpr int kA = C::kStagesA, kB = C::kStagesB, kBars = 2 + 2 * (kA + kB);
+  // stage and phase of position n of a ring
+  auto a_full = [&](int n) { return bar(2 + n % kA); };
+  auto a_empty = [&](int n) { return bar(2 + kA + n % kA); };
+  auto b_full = [&](int n) { return bar(2 + 2 * kA + n % kB); };
+  auto b_empty = [&](int n) { return bar(2 + 2 * kA + kB + n % kB); };
+  auto a_par = [](int n) { return uint32_t(n / kA) & 1u; };
+  auto b_par = [](int n) { return uint32_t(n / kB) & 1u; };
+  const uint32_t s_full = bar(kBars), s_free = bar(kBars + 1), dp_full = bar(kBars + 2),
+                 dp_free = bar(kBars + 3), p_full = bar(kBars + 4), ds_full = bar(kBars + 5),
+                 done = bar(kBars + 8);
+  auto ds_free = [&](int i) { return bar(kBars + 6 + i); };
   const uint32_t sFix[2] = {sbase + C::kOffFixed, sbase + C::kOffFixed + C::kTileBytes};
-  auto sA = [&](int s) { return sbase + C::kOffRingA + s * C::kTileBytes; };
-  auto sB = [&](int s) { return sbase + C::kOffRingB + s * C::kTileBytes; };
+  auto sA = [&](int n) { return sbase + C::kOffRingA + (n % kA) * C::kTileBytes; };
+  auto sB = [&](int n) { return sbase + C::kOffRingB + (n % kB) * C::kTileBytes; };
 
   // ---------------------------------------------- the tiles this unit visits
-  // without ids: a contiguous range; with ids: listed (up to kBwdMaxListed
-  // tiles; beyond, every tile of the range is walked and masked)
+  // without ids: a contiguous range; with ids: the bits of those that share an
+  // id range with the unit's tile (a range of more than kBwdMaxListed tiles is
+  // walked whole, each tile masked)
   BwdWalk walk{nullptr, 0, 0, 0};
   int end;
   if (kKV) {
@@ -310,63 +324,62 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
     }
   }
   int total = max(end - walk.first, 0);
-  if (p.q_sum != nullptr && total <= kBwdMaxListed) {
-    uint16_t* list = reinterpret_cast<uint16_t*>(smem + C::kOffList);
-    int* counts = reinterpret_cast<int*>(smem + C::kOffMisc + 16);   // [12]
+  const int range = total;
+  if (p.q_sum != nullptr && range <= kBwdMaxListed) {
+    uint32_t* bits = reinterpret_cast<uint32_t*>(smem + C::kOffList);
     const int4* mine = (kKV ? p.kv_sum : p.q_sum) +
                        static_cast<int64_t>(b) * (kKV ? p.n_kv_tiles : p.n_q_tiles) + own;
     const int4* other = (kKV ? p.q_sum : p.kv_sum) +
                         static_cast<int64_t>(b) * (kKV ? p.n_q_tiles : p.n_kv_tiles);
     const int4 me = __ldg(mine);
-    int base = 0;
-    for (int t0 = walk.first; t0 < end; t0 += kBwdThreads) {
-      const int t = t0 + int(threadIdx.x);
+    for (int t0 = 32 * warp; t0 < range; t0 += kBwdThreads) {
+      const int t = walk.first + t0 + lane;
       bool act = false, masked = false;
       if (t < end) {
         const int4 o = __ldg(other + t);
         act = !(o.y < me.x || o.x > me.y);
         masked = kKV ? bwd_pair_masked<kKV>(p, b, t, own) : bwd_pair_masked<kKV>(p, b, own, t);
       }
-      const unsigned ballot = __ballot_sync(0xffffffffu, act);
-      if (lane == 0) counts[warp] = __popc(ballot);
-      __syncthreads();
-      int at = base;
-      for (int w = 0; w < kBwdThreads / 32; ++w) {
-        const int n = counts[w];
-        if (w < warp) at += n;
-        base += n;
+      const uint32_t w0 = __ballot_sync(0xffffffffu, act);
+      const uint32_t w1 = __ballot_sync(0xffffffffu, masked);
+      if (lane == 0) {
+        bits[t0 / 32] = w0;
+        bits[kBwdMaxListed / 32 + t0 / 32] = w1;
       }
-      if (act)
-        list[at + __popc(ballot & ((1u << lane) - 1u))] =
-            static_cast<uint16_t>((t - walk.first) | (masked ? kBwdMaskBit : 0));
-      __syncthreads();
     }
-    walk.list = list;
-    total = base;
+    __syncthreads();
+    walk.bits = bits;
+    total = 0;
+    for (int w = 0; w < (range + 31) / 32; ++w) total += __popc(bits[w]);
   }
-  walk.t0 = int((int64_t(total) * split) / n_split);
-  walk.t1 = int((int64_t(total) * (split + 1)) / n_split);
-  const int n_tiles = walk.t1 - walk.t0;
-  auto tile_at = [&](int t) {
-    return walk.first + (walk.list ? walk.list[walk.t0 + t] & (kBwdMaskBit - 1) : walk.t0 + t);
-  };
-  auto masked_at = [&](int t, int tile) {
-    if (walk.list) return (walk.list[walk.t0 + t] & kBwdMaskBit) != 0;
+  const int t0 = int((int64_t(total) * split) / n_split);
+  walk.n = int((int64_t(total) * (split + 1)) / n_split) - t0;
+  walk.start = t0;
+  if (walk.bits != nullptr && walk.n > 0) {   // the position of the t0-th set bit
+    int left = t0, w = 0;
+    for (; left >= __popc(walk.bits[w]); ++w) left -= __popc(walk.bits[w]);
+    uint32_t x = walk.bits[w];
+    for (; left > 0; --left) x &= x - 1u;
+    walk.start = 32 * w + __ffs(x) - 1;
+  }
+  const int n_tiles = walk.n;
+  auto masked_at = [&](int pos) {
+    if (walk.bits) return walk.masked(pos);
+    const int tile = walk.first + pos;
     return kKV ? bwd_pair_masked<kKV>(p, b, tile, own) : bwd_pair_masked<kKV>(p, b, own, tile);
   };
-  auto par = [](int n) { return uint32_t(n / C::kStages) & 1u; };
 
   if (warp == 9) {
     // -------------------------------------------------------------- loads
-    // KV unit: K and V stay; ring A holds Q (and its row statistics), ring B
-    // dO.  Q unit: Q and dO stay; ring A holds K, ring B V.
+    // KV unit: K and V stay; ring A holds Q, ring B dO and the row statistics.
+    // Q unit: Q and dO stay; ring A holds K, ring B V.
     const CUtensorMap* fixed_map[2] = {kKV ? &tm_k : &tm_q, kKV ? &tm_v : &tm_do};
     const CUtensorMap* ring_map[2] = {kKV ? &tm_q : &tm_k, kKV ? &tm_do : &tm_v};
     bool ok = true;
-    int n = 0;
-    for (; n < n_tiles && ok; ++n) {
-      const int st = n % C::kStages;
-      const int tile = tile_at(n);
+    int n_a = 0, n_b = 0;   // loads issued
+    for (int n = 0, pos = walk.start; n < n_tiles && ok; ++n, ++pos) {
+      pos = walk.next(pos);
+      const int tile = walk.first + pos;
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
         if (n == 0) {
@@ -375,46 +388,49 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
             tma_load_3d_elect(sFix[which] + s * C::kSubBytes, fixed_map[which], fixed_full(which),
                               s * 64, own * 128, bh);
         }
-        const uint32_t full = which ? b_full(st) : a_full(st);
-        ok = warp_wait_phase(which ? b_empty(st) : a_empty(st), par(n) ^ 1u, abort_flag, p.err);
+        const uint32_t full = which ? b_full(n) : a_full(n);
+        ok = warp_wait_phase(which ? b_empty(n) : a_empty(n), (which ? b_par(n) : a_par(n)) ^ 1u,
+                             abort_flag, p.err);
         if (!ok) break;
-        const bool with_stats = kKV && which == 0;
+        const bool with_stats = kKV && which == 1;
         mbar_arrive_expect_tx_elect(full, C::kTileBytes + (with_stats ? C::kStatBytes : 0));
-        const uint32_t dst = which ? sB(st) : sA(st);
+        const uint32_t dst = which ? sB(n) : sA(n);
         for (int s = 0; s < C::kSub; ++s)
           tma_load_3d_elect(dst + s * C::kSubBytes, ring_map[which], full, s * 64, tile * 128, bh);
         if (with_stats)
-          bulk_load_elect(sbase + C::kOffStats + st * C::kStatBytes,
+          bulk_load_elect(sbase + C::kOffStats + (n % kB) * C::kStatBytes,
                           p.stats + (static_cast<int64_t>(bh) * p.n_q_tiles + tile) * 256,
                           C::kStatBytes, full);
+        if (which) n_b = n + 1;
+        else n_a = n + 1;
       }
     }
     if (!ok) {
-      // let the loads in flight land before the CTA can exit (every load of
-      // the last kStages positions; a position never issued runs out of time)
+      // let the loads in flight land before the CTA can exit (a wait ends at
+      // the phase of its load, or by its time limit)
       volatile int never = 0;
-      for (int k = max(0, n - 1 - C::kStages); k < n - 1; ++k) {
-        warp_wait_phase(a_full(k % C::kStages), par(k), &never, p.err);
-        warp_wait_phase(b_full(k % C::kStages), par(k), &never, p.err);
-      }
-      warp_wait_phase(a_full((n - 1) % C::kStages), par(n - 1), &never, p.err);
-      warp_wait_phase(fixed_full(0), 0, &never, p.err);
-      warp_wait_phase(fixed_full(1), 0, &never, p.err);
+      for (int k = max(0, n_a - kA); k < n_a; ++k)
+        warp_wait_phase(a_full(k), a_par(k), &never, p.err);
+      for (int k = max(0, n_b - kB); k < n_b; ++k)
+        warp_wait_phase(b_full(k), b_par(k), &never, p.err);
+      for (int which = 0; which < 2; ++which)
+        warp_wait_phase(fixed_full(which), 0, &never, p.err);
     }
     __syncwarp();
   } else if (warp == 8) {
     // -------------------------------------------------------- tensor core
     const uint32_t tS = tmem + C::kTmemS, tDP = tmem + C::kTmemDP;
+    auto wait = [&](uint32_t b_, uint32_t parity) {
+      return warp_wait_phase(b_, parity, abort_flag, p.err);
+    };
     bool ok = true;
     if (n_tiles > 0) {
-      ok = warp_wait_phase(fixed_full(0), 0, abort_flag, p.err) &&
-           warp_wait_phase(a_full(0), 0, abort_flag, p.err);
+      ok = wait(fixed_full(0), 0) && wait(a_full(0), 0);
       if (ok) {
         tc_fence_after();
         bwd_issue_score<D>(tS, sFix[0], sA(0));
         mma_commit_elect(s_full);
-        ok = warp_wait_phase(fixed_full(1), 0, abort_flag, p.err) &&
-             warp_wait_phase(b_full(0), 0, abort_flag, p.err);
+        ok = wait(fixed_full(1), 0) && wait(b_full(0), 0);
       }
       if (ok) {
         tc_fence_after();
@@ -424,55 +440,50 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
       }
     }
     for (int n = 0; n < n_tiles && ok; ++n) {
-      const int st = n % C::kStages, st1 = (n + 1) % C::kStages;
       const bool more = n + 1 < n_tiles;
       const uint32_t tp = uint32_t(n) & 1u;
+      if (more) {   // the next scores, once these are in registers
+        ok = wait(a_full(n + 1), a_par(n + 1)) && wait(s_free, tp);
+        if (!ok) break;
+        tc_fence_after();
+        bwd_issue_score<D>(tS, sFix[0], sA(n + 1));
+        mma_commit_elect(s_full);
+      }
       if (kKV) {
-        // dV += P^T dO_n, S = K Q_{n+1}^T, dK += dS^T Q_n, dP = V dO_{n+1}^T: P
-        // lies over S and dS over dP, whose next product follows in order
-        if (more) ok = warp_wait_phase(a_full(st1), par(n + 1), abort_flag, p.err);
-        ok = ok && warp_wait_phase(p_full, tp, abort_flag, p.err);
+        // dV += P^T dO_n, dK += dS^T Q_n; then dP = V dO_{n+1}^T over both
+        ok = wait(p_full, tp);
         if (!ok) break;
         tc_fence_after();
-        bwd_issue_acc<D>(tmem + C::kTmemAcc0, tS, tS + 64, sB(st), n > 0);
-        mma_commit_elect(b_empty(st));
-        if (more) {
-          bwd_issue_score<D>(tS, sFix[0], sA(st1));
-          mma_commit_elect(s_full);
-          ok = warp_wait_phase(b_full(st1), par(n + 1), abort_flag, p.err);
-        }
-        ok = ok && warp_wait_phase(ds_full, tp, abort_flag, p.err);
+        bwd_issue_acc<D>(tmem + C::kTmemAcc0, tDP, tDP + 64, sB(n), n > 0);
+        ok = wait(ds_full, tp);
         if (!ok) break;
         tc_fence_after();
-        bwd_issue_acc<D>(tmem + C::kTmemAcc1, tDP, tDP + 64, sA(st), n > 0);
-        mma_commit_elect(a_empty(st));
+        bwd_issue_acc<D>(tmem + C::kTmemAcc1, tDP + 32, tDP + 96, sA(n), n > 0);
+        mma_commit_elect(a_empty(n));
+        mma_commit_elect(b_empty(n));   // the statistics were read before ds_full
         if (more) {
-          bwd_issue_score<D>(tDP, sFix[1], sB(st1));
+          ok = wait(b_full(n + 1), b_par(n + 1));
+          if (!ok) break;
+          tc_fence_after();
+          bwd_issue_score<D>(tDP, sFix[1], sB(n + 1));
           mma_commit_elect(dp_full);
         }
       } else {
-        // S = Q K_{n+1}^T once S_n is in registers, dP = dO V_{n+1}^T once
-        // dP_n is, dQ += dS_n K_n
+        // dP = dO V_{n+1}^T once dP_n is in registers, dQ += dS_n K_n
         if (more) {
-          ok = warp_wait_phase(a_full(st1), par(n + 1), abort_flag, p.err) &&
-               warp_wait_phase(s_free, tp, abort_flag, p.err);
+          ok = wait(b_full(n + 1), b_par(n + 1)) && wait(dp_free, tp);
           if (!ok) break;
           tc_fence_after();
-          bwd_issue_score<D>(tS, sFix[0], sA(st1));
-          mma_commit_elect(s_full);
-          ok = warp_wait_phase(b_full(st1), par(n + 1), abort_flag, p.err);
+          bwd_issue_score<D>(tDP, sFix[1], sB(n + 1));
+          mma_commit_elect(dp_full);
+          mma_commit_elect(b_empty(n + 1));
         }
-        ok = ok && warp_wait_phase(ds_full, tp, abort_flag, p.err);
+        ok = wait(ds_full, tp);
         if (!ok) break;
         tc_fence_after();
-        if (more) {
-          bwd_issue_score<D>(tDP, sFix[1], sB(st1));
-          mma_commit_elect(dp_full);
-          mma_commit_elect(b_empty(st1));
-        }
         const uint32_t tDS = tmem + C::kTmemDS + 64u * (n & 1);
-        bwd_issue_acc<D>(tmem + C::kTmemAcc0, tDS, tDS + 32, sA(st), n > 0);
-        mma_commit_elect(a_empty(st));
+        bwd_issue_acc<D>(tmem + C::kTmemAcc0, tDS, tDS + 32, sA(n), n > 0);
+        mma_commit_elect(a_empty(n));
         mma_commit_elect(ds_free(n & 1));
       }
     }
@@ -497,13 +508,13 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
       ndelta = __ldg(st + 128);
     }
     bool ok = true;
-    for (int n = 0; n < n_tiles; ++n) {
-      const int st = n % C::kStages;
+    for (int n = 0, pos = walk.start; n < n_tiles; ++n, ++pos) {
       const uint32_t tp = uint32_t(n) & 1u;
-      const int tile = tile_at(n);
-      const bool masked = masked_at(n, tile);
+      pos = walk.next(pos);
+      const int tile = walk.first + pos;
+      const bool masked = masked_at(pos);
       const float* stats = reinterpret_cast<const float*>(smem + C::kOffStats +
-                                                          st * C::kStatBytes) + 64 * half;
+                                                          (n % kB) * C::kStatBytes) + 64 * half;
       uint64_t vis = ~0ull;
       if (masked) {
         const int x0 = tile * 128 + 64 * half;   // first column's query (KV) or key
@@ -523,43 +534,64 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
         vis = bwd_mask64(x0, lo, hi, ids, kKV ? p.S_q : p.S_kv, my_id);
       }
       if (kKV) {   // the statistics of this query tile have landed
-        ok = warp_wait_phase(a_full(st), par(n), abort_flag, p.err);
+        ok = warp_wait_phase(b_full(n), b_par(n), abort_flag, p.err);
         if (!ok) break;
       }
       ok = warp_wait_phase(s_full, tp, abort_flag, p.err);
       if (!ok) break;
       tc_fence_after();
       float pr[64];
-      bwd_probs<kEmu, kKV>(tS, p.c, nlse, stats, pr);
+      bwd_probs<kEmu, kKV>(tS, p.c, nlse, stats, s_free, pr);
       if (masked) {
 #pragma unroll
         for (int x = 0; x < 64; ++x) pr[x] = (vis >> x) & 1 ? pr[x] : 0.f;
       }
-      uint32_t pk[32];
+      uint32_t r[32], pk[16];
       if (kKV) {
+        uint32_t pp[32];
 #pragma unroll
-        for (int x = 0; x < 32; ++x) pk[x] = pack_bf16x2(pr[2 * x], pr[2 * x + 1]);
-        tmem_st32(tS, pk);
+        for (int x = 0; x < 32; ++x) pp[x] = pack_bf16x2(pr[2 * x], pr[2 * x + 1]);
+        ok = warp_wait_phase(dp_full, tp, abort_flag, p.err);
+        if (!ok) break;
+        tc_fence_after();
+        // P goes over the first 32 columns of dP, dS over the other 32, each
+        // once they are in registers
+        tmem_ld32(tDP, r);
+        tmem_ld_wait();
+        reg_fence(r);
+        tmem_st32(tDP, pp);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(p_full);
+        bwd_dscores32<true>(r, 0.f, stats + 128, pr, pk);
+        tmem_ld32(tDP + 32, r);
+        tmem_ld_wait();
+        reg_fence(r);
+        tmem_st16(tDP + 32, pk);
+        bwd_dscores32<true>(r, 0.f, stats + 160, pr + 32, pk);
+        tmem_st16(tDP + 48, pk);
       } else {
+        ok = warp_wait_phase(dp_full, tp, abort_flag, p.err);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t r1[32], pk1[16];
+        tmem_ld32(tDP, r);
+        tmem_ld32(tDP + 32, r1);
+        tmem_ld_wait();
+        reg_fence(r);
+        reg_fence(r1);
         tc_fence_before();
-        mbar_arrive(s_free);
-      }
-      ok = warp_wait_phase(dp_full, tp, abort_flag, p.err);
-      if (!ok) break;
-      tc_fence_after();
-      bwd_dscores<kKV>(tDP, ndelta, stats + 128, pr, pk);
-      if (kKV) {
-        tmem_st32(tDP, pk);
-      } else {
+        mbar_arrive(dp_free);
+        bwd_dscores32<false>(r, ndelta, nullptr, pr, pk);
+        bwd_dscores32<false>(r1, ndelta, nullptr, pr + 32, pk1);
         if (n >= 2) {   // dQ's product of two tiles ago has read this buffer
           ok = warp_wait_phase(ds_free(n & 1), uint32_t((n >> 1) - 1) & 1u, abort_flag, p.err);
           if (!ok) break;
           tc_fence_after();
         }
-        tmem_st32(tmem + lane_off + C::kTmemDS + 64u * (n & 1) + 32u * half, pk);
+        const uint32_t dst = tmem + lane_off + C::kTmemDS + 64u * (n & 1) + 32u * half;
+        tmem_st16(dst, pk);
+        tmem_st16(dst + 16, pk1);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -602,20 +634,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                        const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ CUtensorMap tm_do, const BwdParams p) {
   using C = BwdCfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw_base = smem_u32(smem_raw);
-  const uint32_t sbase = (raw_base + 1023u) & ~1023u;
-  uint8_t* smem = smem_raw + (sbase - raw_base);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t sbase = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw;
   // a wait of an earlier CTA timed out: the results are already invalid
   if (*reinterpret_cast<volatile int*>(p.err) != 0) return;
+  if (sbase & 1023u) {   // the tiles' swizzle needs the alignment asked for above
+    if (threadIdx.x == 0) atomicOr(p.err, kErrTimeout);
+    return;
+  }
 
   const int warp = threadIdx.x >> 5;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   if (threadIdx.x == 0) {
     auto bar = [&](int i) { return sbase + C::kOffBar + 8 * i; };
-    constexpr int kB0 = 2 + 4 * C::kStages;
+    constexpr int kBars = 2 + 2 * (C::kStagesA + C::kStagesB);
     for (int i = 0; i < C::kNumBars; ++i) {
-      const bool many = i == kB0 + 1 || i == kB0 + 2 || i == kB0 + 4;   // s_free p_full ds_full
+      // s_free, dp_free, p_full, ds_full: every softmax thread arrives
+      const bool many = i == kBars + 1 || (i >= kBars + 3 && i <= kBars + 5);
       mbar_init(bar(i), many ? 256 : 1);
     }
     *reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4) = 0;
