@@ -17,10 +17,9 @@
 // time.  P and dS go from registers straight to tensor memory, as the A
 // operand of the product that consumes them, and never touch shared memory.
 //
-// 384 threads: warps 0-7 compute P and dS (warp w holds TMEM lanes
-// 32 (w % 4) + [0, 32), columns 64 (w / 4) + [0, 64) of each score tile), warp
-// 8 issues the tcgen05.mma, warp 9 the TMA loads, warps 10-11 only help to
-// list the visited tiles.
+// 640 threads: warps 0-15 compute P and dS, 32 columns of a tile row a thread
+// at a time (warp w: TMEM lanes 32 (w % 4) + [0, 32)); warp 16 issues the
+// tcgen05.mma, warp 17 the TMA loads.
 #pragma once
 #include <climits>
 #include <cstdint>
@@ -31,7 +30,9 @@
 
 namespace vidattn {
 
-constexpr int kBwdThreads = 384;
+constexpr int kBwdSoftmaxWarps = 16;
+constexpr int kBwdMmaWarp = 16, kBwdLoadWarp = 17;
+constexpr int kBwdThreads = 640;   // 2 warps more: registers are dealt to 4 warps at a time
 constexpr int kBwdMaxListed = 3072;   // tiles of a unit's range whose visits are kept as bits
 
 struct BwdParams {
@@ -69,26 +70,36 @@ struct BwdCfg {
   // whole step, so that ring has one stage more (with 2 a load had to land
   // between two products: 3500 cycles a step instead of 2100).  At D = 128
   // the seven tiles leave 3 KB for everything else.
-  static constexpr int kStagesA = 3, kStagesB = 2;
+  static constexpr int kStagesA = D == 128 ? 3 : 4, kStagesB = D == 128 ? 2 : 3;
   static constexpr int kOffFixed = 0;
   static constexpr int kOffRingA = 2 * kTileBytes;
   static constexpr int kOffRingB = kOffRingA + kStagesA * kTileBytes;
   static constexpr int kOffStats = kOffRingB + kStagesB * kTileBytes;   // [kStagesB][2][128] fp32
   static constexpr int kStatBytes = 2 * 128 * 4;
   static constexpr int kOffBar = kOffStats + kStagesB * kStatBytes;
-  // fixed_full[2] a_full[] a_empty[] b_full[] b_empty[] s_full s_free
-  // dp_full dp_free p_full ds_full ds_free[2] done
-  static constexpr int kNumBars = 2 + 2 * (kStagesA + kStagesB) + 9;
+  // fixed_full[2] a_full[] a_empty[] b_full[] b_empty[] s_full dp_full[2]
+  // done s_free p_full ds_full; the last three take an arrival of each softmax
+  // warp
+  static constexpr int kNumBars = 2 + 2 * (kStagesA + kStagesB) + 7;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;   // tmem addr, abort flag
   static constexpr int kOffList = kOffMisc + 16;            // visited tiles, masked tiles: bits
   static constexpr int kSmemBytes = kOffList + 2 * kBwdMaxListed / 8;
   static_assert(kSmemBytes <= 227 * 1024, "one CTA's shared memory on sm_100");
   static constexpr uint32_t kTmemCols = 512;
-  // KV units: dV [0,D), dK [128,128+D), S [256,384), dP [384,512), and over
-  // the dP columns [64h, 64h + 64) of half h, once read, P and dS (32 each).
-  // Q units: dQ [0,D), dS buffers [128,192) and [192,256), S [256,384), dP [384,512).
-  static constexpr uint32_t kTmemAcc0 = 0, kTmemAcc1 = 128, kTmemDS = 128, kTmemS = 256,
-                            kTmemDP = 384;
+  // Columns of tensor memory: dV (or dQ), dK, the scores S, and one or two dP
+  // tiles; over a dP tile, once it is read, go P and dS (16 columns each per 32
+  // of dP).  S is free for the next tile's scores as soon as it is in
+  // registers.  With two dP tiles the next dP is computed beside the softmax
+  // as well; a KV unit at D = 128 has room for one.
+  static __host__ __device__ constexpr int dp_tiles(bool kv) { return kv && D == 128 ? 1 : 2; }
+  static constexpr uint32_t kTmemAcc0 = 0;
+  static constexpr uint32_t kTmemAcc1 = D;
+  static __host__ __device__ constexpr uint32_t tmem_dp(bool kv, int n) {
+    return 384u - 128u * ((n + 1) % dp_tiles(kv));
+  }
+  static __host__ __device__ constexpr uint32_t tmem_s(bool kv) {
+    return 384u - 128u * dp_tiles(kv);
+  }
   static constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0);
   static constexpr uint32_t kIdescAcc = idesc_bf16_f32(128, D, 0, 1);
 };
@@ -105,18 +116,30 @@ __device__ __forceinline__ void bwd_issue_score(uint32_t d_tmem, uint32_t sA, ui
   }
 }
 
-// Acc[128 x D] += A[128 x 128] B[128 x D]: A bf16 in tensor memory (rows
-// [0,64) of the contraction at a_lo, [64,128) at a_hi), B a shared tile.
+// Acc[128 x D] += A[128 x 128] B[128 x D]: A bf16 in tensor memory, 32 values
+// of a row in 16 columns, the next 32 from 32 columns on; B a shared tile.
 template <int D>
-__device__ __forceinline__ void bwd_issue_acc(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi,
-                                              uint32_t sB, bool accumulate) {
+__device__ __forceinline__ void bwd_issue_acc(uint32_t d_tmem, uint32_t a_tmem, uint32_t sB,
+                                              bool accumulate) {
   using C = BwdCfg<D>;
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk) {
     const uint64_t b = smem_desc_sw128(sB + kk * 2048, C::kSubBytes, 1024);
-    const uint32_t a = (kk < 4) ? a_lo + kk * 8 : a_hi + (kk - 4) * 8;
-    mma_ts_elect(d_tmem, a, b, C::kIdescAcc, (accumulate || kk > 0) ? 1u : 0u);
+    mma_ts_elect(d_tmem, a_tmem + (kk / 2) * 32 + (kk % 2) * 8, b, C::kIdescAcc,
+                 (accumulate || kk > 0) ? 1u : 0u);
   }
+}
+
+// warp_wait_phase with its polling loop out of line: the phase has often
+// passed already, and the kernel waits in many places.
+static __device__ __noinline__ bool bwd_wait_slow(uint32_t bar, uint32_t parity,
+                                                  volatile int* abort_flag, int* err) {
+  return warp_wait_phase(bar, parity, abort_flag, err);
+}
+__device__ __forceinline__ bool bwd_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                         int* err) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return bwd_wait_slow(bar, parity, abort_flag, err);
 }
 
 // Untiled bulk copy into shared memory (16-byte aligned, size a multiple of 16).
@@ -163,50 +186,42 @@ __device__ __forceinline__ bool bwd_pair_masked(const BwdParams& p, int b, int i
   return masked;
 }
 
-// Which of the 64 columns [x0, x0 + 64) of a score tile row are visible, as
+// Which of the 32 columns [x0, x0 + 32) of a score tile row are visible, as
 // bits: lo <= column < hi, and the column's id equal to the row's.
-__device__ __forceinline__ uint64_t bwd_mask64(int x0, int lo, int hi, const int32_t* ids,
-                                               int n_ids, int my_id) {
-  uint64_t m = 0;
-  const int a = max(lo - x0, 0), e = min(hi - x0, 64);
-  if (a < e) m = (~0ull >> (64 - (e - a))) << a;
-  if (ids != nullptr) {
-    uint64_t eq = 0;
-    for (int x = 0; x < 64; ++x) {
+static __device__ __noinline__ uint32_t bwd_mask32(int x0, int lo, int hi, const int32_t* ids,
+                                                  int n_ids, int my_id) {
+  uint32_t m = 0;
+  const int a = max(lo - x0, 0), e = min(hi - x0, 32);
+  if (a < e) m = (~0u >> (32 - (e - a))) << a;
+  if (ids != nullptr && m != 0u) {
+    uint32_t eq = 0;
+#pragma unroll 8
+    for (int x = 0; x < 32; ++x) {
       const int col = x0 + x;
       const int id = col < n_ids ? __ldg(ids + col) : 0;
-      if (id == my_id) eq |= 1ull << x;
+      if (id == my_id) eq |= 1u << x;
     }
     m &= eq;
   }
   return m;
 }
 
-// One thread's 64 columns of a score tile row to probabilities: 2^(c s + off),
-// off the row's (kPerColumn false) or read per column from shared memory.  Of
-// every 16, the last kEmu on the FMA pipe.
+// 32 scores of a row (r) to probabilities: 2^(c s + off), off the row's
+// (kPerColumn false) or read per column from shared memory.  Of every 16, the
+// last kEmu on the FMA pipe.
 template <int kEmu, bool kPerColumn>
-__device__ __forceinline__ void bwd_probs(uint32_t taddr, float c, float off, const float* offs,
-                                          uint32_t free_bar, float (&pr)[64]) {
-  uint32_t r[2][32];
-  tmem_ld32(taddr, r[0]);
-  tmem_ld32(taddr + 32, r[1]);
-  tmem_ld_wait();
-  reg_fence(r[0]);
-  reg_fence(r[1]);
-  tc_fence_before();
-  mbar_arrive(free_bar);   // the scores are in registers
+__device__ __forceinline__ void bwd_probs32(const uint32_t (&r)[32], float c, float off,
+                                            const float* offs, float (&pr)[32]) {
   const float2 c2 = make_float2(c, c);
 #pragma unroll
-  for (int x = 0; x < 64; x += 4) {
+  for (int x = 0; x < 32; x += 4) {
     float4 o = make_float4(off, off, off, off);
     if (kPerColumn) o = *reinterpret_cast<const float4*>(offs + x);
 #pragma unroll
     for (int y = 0; y < 4; y += 2) {
       const int e = x + y;
-      const float2 arg = ffma2(make_float2(__uint_as_float(r[e >> 5][e & 31]),
-                                           __uint_as_float(r[e >> 5][(e & 31) + 1])),
-                               c2, y == 0 ? make_float2(o.x, o.y) : make_float2(o.z, o.w));
+      const float2 arg = ffma2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), c2,
+                               y == 0 ? make_float2(o.x, o.y) : make_float2(o.z, o.w));
       float2 v;
       if ((e & 15) < 16 - kEmu) {
         v.x = ex2(arg.x);
@@ -220,10 +235,10 @@ __device__ __forceinline__ void bwd_probs(uint32_t taddr, float c, float off, co
   }
 }
 
-// dS = P (dP - delta) of 32 columns (r: dP), packed to bf16 pairs.
+// dS = P (dP - delta) of the same 32 columns (r: dP), packed to bf16 pairs.
 template <bool kPerColumn>
 __device__ __forceinline__ void bwd_dscores32(const uint32_t (&r)[32], float nd, const float* nds,
-                                              const float* pr, uint32_t (&pk)[16]) {
+                                              const float (&pr)[32], uint32_t (&pk)[16]) {
 #pragma unroll
   for (int x = 0; x < 32; x += 4) {
     float4 o = make_float4(nd, nd, nd, nd);
@@ -239,13 +254,13 @@ __device__ __forceinline__ void bwd_dscores32(const uint32_t (&r)[32], float nd,
   }
 }
 
-// One row of an accumulator from tensor memory, times mul, to bf16 (out) or
+// kCols columns of an accumulator's row from tensor memory, times mul, to bf16 (out) or
 // to fp32 (part).  have: the accumulator was written (a tile was visited).
-template <int D>
+template <int kCols>
 __device__ __forceinline__ void bwd_store_row(uint32_t taddr, bool have, bool row_valid, float mul,
                                               uint16_t* out, float* part) {
 #pragma unroll 1
-  for (int kk = 0; kk < D / 32; ++kk) {
+  for (int kk = 0; kk < kCols / 32; ++kk) {
     uint32_t o[32];
     if (have) {
       tmem_ld32(taddr + 32 * kk, o);
@@ -296,10 +311,11 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
   auto b_empty = [&](int n) { return bar(2 + 2 * kA + kB + n % kB); };
   auto a_par = [](int n) { return uint32_t(n / kA) & 1u; };
   auto b_par = [](int n) { return uint32_t(n / kB) & 1u; };
-  const uint32_t s_full = bar(kBars), s_free = bar(kBars + 1), dp_full = bar(kBars + 2),
-                 dp_free = bar(kBars + 3), p_full = bar(kBars + 4), ds_full = bar(kBars + 5),
-                 done = bar(kBars + 8);
-  auto ds_free = [&](int i) { return bar(kBars + 6 + i); };
+  constexpr int kX = C::dp_tiles(kKV);
+  const uint32_t s_full = bar(kBars), done = bar(kBars + 3), s_free = bar(kBars + 4),
+                 p_full = bar(kBars + 5), ds_full = bar(kBars + 6);
+  auto dp_full = [&](int n) { return bar(kBars + 1 + n % kX); };
+  auto dp_par = [](int n) { return uint32_t(n / kX) & 1u; };
   const uint32_t sFix[2] = {sbase + C::kOffFixed, sbase + C::kOffFixed + C::kTileBytes};
   auto sA = [&](int n) { return sbase + C::kOffRingA + (n % kA) * C::kTileBytes; };
   auto sB = [&](int n) { return sbase + C::kOffRingB + (n % kB) * C::kTileBytes; };
@@ -363,13 +379,23 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
     walk.start = 32 * w + __ffs(x) - 1;
   }
   const int n_tiles = walk.n;
-  auto masked_at = [&](int pos) {
+  // without ids the masked tiles are the first ones of a KV unit, the last
+  // ones of a Q unit; ids beyond the bits: all
+  int edge;
+  if (kKV) {
+    edge = p.causal ? (own * 128 + 127 - p.causal_off + 127) / 128 : 0;
+    if (p.q_sum) edge = INT_MAX;
+  } else {
+    edge = (p.S_kv & 127) ? p.n_kv_tiles - 1 : p.n_kv_tiles;
+    if (p.causal) edge = min(edge, max((own * 128 + p.causal_off + 1) >> 7, 0));
+    if (p.q_sum) edge = 0;
+  }
+  auto masked_at = [&](int pos, int tile) {
     if (walk.bits) return walk.masked(pos);
-    const int tile = walk.first + pos;
-    return kKV ? bwd_pair_masked<kKV>(p, b, tile, own) : bwd_pair_masked<kKV>(p, b, own, tile);
+    return kKV ? tile < edge : tile >= edge;
   };
 
-  if (warp == 9) {
+  if (warp == kBwdLoadWarp) {
     // -------------------------------------------------------------- loads
     // KV unit: K and V stay; ring A holds Q, ring B dO and the row statistics.
     // Q unit: Q and dO stay; ring A holds K, ring B V.
@@ -417,75 +443,51 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
         warp_wait_phase(fixed_full(which), 0, &never, p.err);
     }
     __syncwarp();
-  } else if (warp == 8) {
+  } else if (warp == kBwdMmaWarp) {
     // -------------------------------------------------------- tensor core
-    const uint32_t tS = tmem + C::kTmemS, tDP = tmem + C::kTmemDP;
     auto wait = [&](uint32_t b_, uint32_t parity) {
-      return warp_wait_phase(b_, parity, abort_flag, p.err);
+      return bwd_wait(b_, parity, abort_flag, p.err);
+    };
+    // scores of tile n, dP of tile n
+    auto scores = [&](int n) {
+      if (!wait(a_full(n), a_par(n))) return false;
+      tc_fence_after();
+      bwd_issue_score<D>(tmem + C::tmem_s(kKV), sFix[0], sA(n));
+      mma_commit_elect(s_full);
+      return true;
+    };
+    auto dprobs = [&](int n) {
+      if (!wait(b_full(n), b_par(n))) return false;
+      tc_fence_after();
+      bwd_issue_score<D>(tmem + C::tmem_dp(kKV, n), sFix[1], sB(n));
+      mma_commit_elect(dp_full(n));
+      if (!kKV) mma_commit_elect(b_empty(n));
+      return true;
     };
     bool ok = true;
-    if (n_tiles > 0) {
-      ok = wait(fixed_full(0), 0) && wait(a_full(0), 0);
-      if (ok) {
-        tc_fence_after();
-        bwd_issue_score<D>(tS, sFix[0], sA(0));
-        mma_commit_elect(s_full);
-        ok = wait(fixed_full(1), 0) && wait(b_full(0), 0);
-      }
-      if (ok) {
-        tc_fence_after();
-        bwd_issue_score<D>(tDP, sFix[1], sB(0));
-        mma_commit_elect(dp_full);
-        if (!kKV) mma_commit_elect(b_empty(0));
-      }
-    }
+    if (n_tiles > 0) ok = wait(fixed_full(0), 0) && scores(0) && wait(fixed_full(1), 0) && dprobs(0);
     for (int n = 0; n < n_tiles && ok; ++n) {
       const bool more = n + 1 < n_tiles;
       const uint32_t tp = uint32_t(n) & 1u;
-      if (more) {   // the next scores, once these are in registers
-        ok = wait(a_full(n + 1), a_par(n + 1)) && wait(s_free, tp);
+      const uint32_t tX = tmem + C::tmem_dp(kKV, n);
+      // the next scores once these are in registers, and, into the other dP
+      // tile (whose P and dS the products of tile n - 1 have read), the next dP
+      if (more) ok = wait(s_free, tp) && scores(n + 1);
+      if (more && kX == 2) ok = ok && dprobs(n + 1);
+      if (kKV && kX == 1) {   // P is ready before dS
+        ok = ok && wait(p_full, tp);
         if (!ok) break;
         tc_fence_after();
-        bwd_issue_score<D>(tS, sFix[0], sA(n + 1));
-        mma_commit_elect(s_full);
+        bwd_issue_acc<D>(tmem + C::kTmemAcc0, tX, sB(n), n > 0);
       }
-      if (kKV) {
-        // dV += P^T dO_n, dK += dS^T Q_n; then dP = V dO_{n+1}^T over both
-        ok = wait(p_full, tp);
-        if (!ok) break;
-        tc_fence_after();
-        bwd_issue_acc<D>(tmem + C::kTmemAcc0, tDP, tDP + 64, sB(n), n > 0);
-        ok = wait(ds_full, tp);
-        if (!ok) break;
-        tc_fence_after();
-        bwd_issue_acc<D>(tmem + C::kTmemAcc1, tDP + 32, tDP + 96, sA(n), n > 0);
-        mma_commit_elect(a_empty(n));
-        mma_commit_elect(b_empty(n));   // the statistics were read before ds_full
-        if (more) {
-          ok = wait(b_full(n + 1), b_par(n + 1));
-          if (!ok) break;
-          tc_fence_after();
-          bwd_issue_score<D>(tDP, sFix[1], sB(n + 1));
-          mma_commit_elect(dp_full);
-        }
-      } else {
-        // dP = dO V_{n+1}^T once dP_n is in registers, dQ += dS_n K_n
-        if (more) {
-          ok = wait(b_full(n + 1), b_par(n + 1)) && wait(dp_free, tp);
-          if (!ok) break;
-          tc_fence_after();
-          bwd_issue_score<D>(tDP, sFix[1], sB(n + 1));
-          mma_commit_elect(dp_full);
-          mma_commit_elect(b_empty(n + 1));
-        }
-        ok = wait(ds_full, tp);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t tDS = tmem + C::kTmemDS + 64u * (n & 1);
-        bwd_issue_acc<D>(tmem + C::kTmemAcc0, tDS, tDS + 32, sA(n), n > 0);
-        mma_commit_elect(a_empty(n));
-        mma_commit_elect(ds_free(n & 1));
-      }
+      ok = ok && wait(ds_full, tp);
+      if (!ok) break;
+      tc_fence_after();
+      if (kKV && kX == 2) bwd_issue_acc<D>(tmem + C::kTmemAcc0, tX, sB(n), n > 0);
+      bwd_issue_acc<D>(tmem + (kKV ? C::kTmemAcc1 : C::kTmemAcc0), tX + 16, sA(n), n > 0);
+      mma_commit_elect(a_empty(n));
+      if (kKV) mma_commit_elect(b_empty(n));   // the statistics were read before ds_full
+      if (more && kX == 1) ok = dprobs(n + 1);   // over P and dS
     }
     // every product issued has finished before the epilogue and the release
     // of tensor memory
@@ -493,131 +495,113 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
     volatile int never = 0;
     warp_wait_phase(done, 0, &never, p.err);
     __syncwarp();
-  } else if (warp < 8) {
+  } else if (warp < kBwdSoftmaxWarps) {
     // --------------------------------------------------------- P and dS
-    const int half = warp >> 2;
+    const int quarter = warp >> 2;   // of a tile's columns
+    const int x0 = 32 * quarter;
     const int r = ((warp & 3) << 5) + lane;
-    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lane_off + C::kTmemS + 64u * half;
-    const uint32_t tDP = tmem + lane_off + C::kTmemDP + 64u * half;
+    const uint32_t tLane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t tS = tLane + C::tmem_s(kKV) + x0;
     const int row = own * 128 + r;   // this thread's key (KV) or query row
+    // one arrival a warp, after all its lanes
+    auto arrive = [&](uint32_t b_) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_);
+    };
+    auto wait = [&](uint32_t b_, uint32_t parity) {
+      const bool ok = bwd_wait(b_, parity, abort_flag, p.err);
+      tc_fence_after();
+      return ok;
+    };
     float nlse = 0.f, ndelta = 0.f;
     if (!kKV) {
       const float* st = p.stats + (static_cast<int64_t>(bh) * p.n_q_tiles + own) * 256 + r;
       nlse = __ldg(st);
       ndelta = __ldg(st + 128);
     }
+    // which of the 32 columns from x0 on (queries of a KV unit, keys of a Q
+    // unit) this thread's row sees
+    auto visible = [&](int x0) {
+      int lo = 0, hi = kKV ? p.S_q : p.S_kv;
+      if (p.causal) {
+        if (kKV) lo = row - p.causal_off;
+        else hi = min(hi, row + p.causal_off + 1);
+      }
+      const int32_t* ids = nullptr;
+      int my_id = 0;
+      if (p.q_sum) {
+        const int32_t* own_ids = kKV ? p.seg_kv : p.seg_q;
+        const int n_own = kKV ? p.S_kv : p.S_q;
+        ids = (kKV ? p.seg_q : p.seg_kv) + static_cast<int64_t>(b) * (kKV ? p.S_q : p.S_kv);
+        if (row < n_own) my_id = __ldg(own_ids + static_cast<int64_t>(b) * n_own + row);
+      }
+      return bwd_mask32(x0, lo, hi, ids, kKV ? p.S_q : p.S_kv, my_id);
+    };
     bool ok = true;
-    for (int n = 0, pos = walk.start; n < n_tiles; ++n, ++pos) {
-      const uint32_t tp = uint32_t(n) & 1u;
-      pos = walk.next(pos);
+    int pos = walk.start - 1;
+    for (int n = 0; n < n_tiles; ++n) {
+      pos = walk.next(pos + 1);
       const int tile = walk.first + pos;
-      const bool masked = masked_at(pos);
-      const float* stats = reinterpret_cast<const float*>(smem + C::kOffStats +
-                                                          (n % kB) * C::kStatBytes) + 64 * half;
-      uint64_t vis = ~0ull;
-      if (masked) {
-        const int x0 = tile * 128 + 64 * half;   // first column's query (KV) or key
-        int lo = 0, hi = kKV ? p.S_q : p.S_kv;
-        if (p.causal) {
-          if (kKV) lo = row - p.causal_off;
-          else hi = min(hi, row + p.causal_off + 1);
-        }
-        const int32_t* ids = nullptr;
-        int my_id = 0;
-        if (p.q_sum) {
-          const int32_t* own_ids = kKV ? p.seg_kv : p.seg_q;
-          const int n_own = kKV ? p.S_kv : p.S_q;
-          ids = (kKV ? p.seg_q : p.seg_kv) + static_cast<int64_t>(b) * (kKV ? p.S_q : p.S_kv);
-          if (row < n_own) my_id = __ldg(own_ids + static_cast<int64_t>(b) * n_own + row);
-        }
-        vis = bwd_mask64(x0, lo, hi, ids, kKV ? p.S_q : p.S_kv, my_id);
-      }
-      if (kKV) {   // the statistics of this query tile have landed
-        ok = warp_wait_phase(b_full(n), b_par(n), abort_flag, p.err);
-        if (!ok) break;
-      }
-      ok = warp_wait_phase(s_full, tp, abort_flag, p.err);
+      const bool masked = masked_at(pos, tile);
+      const uint32_t vis = masked ? visible(tile * 128 + x0) : ~0u;
+      const uint32_t tX = tLane + C::tmem_dp(kKV, n) + x0;
+      const float* stats =
+          reinterpret_cast<const float*>(smem + C::kOffStats + (n % kB) * C::kStatBytes) + x0;
+      // the statistics of this query tile, then its scores
+      if (kKV) ok = wait(b_full(n), b_par(n));
+      ok = ok && wait(s_full, uint32_t(n) & 1u);
       if (!ok) break;
-      tc_fence_after();
-      float pr[64];
-      bwd_probs<kEmu, kKV>(tS, p.c, nlse, stats, s_free, pr);
+      uint32_t rr[32], pk[16];
+      float pr[32];
+      tmem_ld32(tS, rr);
+      tmem_ld_wait();
+      reg_fence(rr);
+      arrive(s_free);
+      bwd_probs32<kEmu, kKV>(rr, p.c, nlse, stats, pr);
       if (masked) {
 #pragma unroll
-        for (int x = 0; x < 64; ++x) pr[x] = (vis >> x) & 1 ? pr[x] : 0.f;
+        for (int x = 0; x < 32; ++x) pr[x] = (vis >> x) & 1 ? pr[x] : 0.f;
       }
-      uint32_t r[32], pk[16];
       if (kKV) {
-        uint32_t pp[32];
 #pragma unroll
-        for (int x = 0; x < 32; ++x) pp[x] = pack_bf16x2(pr[2 * x], pr[2 * x + 1]);
-        ok = warp_wait_phase(dp_full, tp, abort_flag, p.err);
-        if (!ok) break;
-        tc_fence_after();
-        // P goes over the first 32 columns of dP, dS over the other 32, each
-        // once they are in registers
-        tmem_ld32(tDP, r);
-        tmem_ld_wait();
-        reg_fence(r);
-        tmem_st32(tDP, pp);
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(p_full);
-        bwd_dscores32<true>(r, 0.f, stats + 128, pr, pk);
-        tmem_ld32(tDP + 32, r);
-        tmem_ld_wait();
-        reg_fence(r);
-        tmem_st16(tDP + 32, pk);
-        bwd_dscores32<true>(r, 0.f, stats + 160, pr + 32, pk);
-        tmem_st16(tDP + 48, pk);
-      } else {
-        ok = warp_wait_phase(dp_full, tp, abort_flag, p.err);
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t r1[32], pk1[16];
-        tmem_ld32(tDP, r);
-        tmem_ld32(tDP + 32, r1);
-        tmem_ld_wait();
-        reg_fence(r);
-        reg_fence(r1);
-        tc_fence_before();
-        mbar_arrive(dp_free);
-        bwd_dscores32<false>(r, ndelta, nullptr, pr, pk);
-        bwd_dscores32<false>(r1, ndelta, nullptr, pr + 32, pk1);
-        if (n >= 2) {   // dQ's product of two tiles ago has read this buffer
-          ok = warp_wait_phase(ds_free(n & 1), uint32_t((n >> 1) - 1) & 1u, abort_flag, p.err);
-          if (!ok) break;
-          tc_fence_after();
-        }
-        const uint32_t dst = tmem + lane_off + C::kTmemDS + 64u * (n & 1) + 32u * half;
-        tmem_st16(dst, pk);
-        tmem_st16(dst + 16, pk1);
+        for (int x = 0; x < 16; ++x) pk[x] = pack_bf16x2(pr[2 * x], pr[2 * x + 1]);
       }
+      ok = wait(dp_full(n), dp_par(n));
+      if (!ok) break;
+      tmem_ld32(tX, rr);
+      tmem_ld_wait();
+      reg_fence(rr);
+      if (kKV) tmem_st16(tX, pk);   // over the dP just read
+      if (kKV && kX == 1) {
+        tmem_st_wait();
+        arrive(p_full);
+      }
+      bwd_dscores32<kKV>(rr, ndelta, stats + 128, pr, pk);
+      tmem_st16(tX + 16, pk);
       tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(ds_full);
+      arrive(ds_full);
     }
     // ------------------------------------------------------------ epilogue
     ok = ok && warp_wait_phase(done, 0, abort_flag, p.err);
     if (ok) {
       tc_fence_after();
       const bool have = n_tiles > 0;
-      if (kKV) {   // one half writes dV, the other dK
-        const bool valid = row < p.S_kv;
-        const int64_t at = (static_cast<int64_t>(bh) * p.S_kv + row) * D;
+      if (kKV) {   // a quarter of the warps each: the halves of dV's and of dK's columns
+        const bool dk = quarter >= 2;
+        const int col = (quarter & 1) * (D / 2);
+        const int64_t at = (static_cast<int64_t>(bh) * p.S_kv + row) * D + col;
         float* part = nullptr;
         if (n_split > 1)
-          part = p.part_kv + (int64_t(split) * 2 + (half ? 0 : 1)) * p.BH * p.S_kv * D + at;
-        if (half == 0)
-          bwd_store_row<D>(tmem + lane_off + C::kTmemAcc0, have, valid, 1.f, p.dv + at, part);
-        else
-          bwd_store_row<D>(tmem + lane_off + C::kTmemAcc1, have, valid, p.scale, p.dk + at, part);
-      } else if (half == 0) {
-        const int64_t at = (static_cast<int64_t>(bh) * p.S_q + row) * D;
+          part = p.part_kv + (int64_t(split) * 2 + (dk ? 0 : 1)) * p.BH * p.S_kv * D + at;
+        bwd_store_row<D / 2>(tLane + (dk ? C::kTmemAcc1 : C::kTmemAcc0) + col, have, row < p.S_kv,
+                             dk ? p.scale : 1.f, (dk ? p.dk : p.dv) + at, part);
+      } else if (quarter < D / 32) {   // 32 of dQ's columns each
+        const int col = 32 * quarter;
+        const int64_t at = (static_cast<int64_t>(bh) * p.S_q + row) * D + col;
         float* part = nullptr;
         if (n_split > 1) part = p.part_q + int64_t(split) * p.BH * p.S_q * D + at;
-        bwd_store_row<D>(tmem + lane_off + C::kTmemAcc0, have, row < p.S_q, p.scale, p.dq + at,
-                         part);
+        bwd_store_row<32>(tLane + C::kTmemAcc0 + col, have, row < p.S_q, p.scale, p.dq + at, part);
       }
     }
   }
@@ -650,14 +634,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     auto bar = [&](int i) { return sbase + C::kOffBar + 8 * i; };
     constexpr int kBars = 2 + 2 * (C::kStagesA + C::kStagesB);
     for (int i = 0; i < C::kNumBars; ++i) {
-      // s_free, dp_free, p_full, ds_full: every softmax thread arrives
-      const bool many = i == kBars + 1 || (i >= kBars + 3 && i <= kBars + 5);
-      mbar_init(bar(i), many ? 256 : 1);
+      mbar_init(bar(i), i >= kBars + 4 ? kBwdSoftmaxWarps : 1);
     }
     *reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4) = 0;
     fence_mbar_init();
   }
-  if (warp == 8) {
+  if (warp == kBwdMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
     tmem_relinquish();
   }
@@ -683,7 +665,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kBwdMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
