@@ -78,9 +78,11 @@ struct BwdCfg {
   static constexpr int kStatBytes = 2 * 128 * 4;
   static constexpr int kOffBar = kOffStats + kStagesB * kStatBytes;
   // fixed_full[2] a_full[] a_empty[] b_full[] b_empty[] s_full dp_full[2]
-  // done s_free p_full ds_full; the last three take an arrival of each softmax
-  // warp
-  static constexpr int kNumBars = 2 + 2 * (kStagesA + kStagesB) + 7;
+  // done s_free p_full ds_full[2]; the last four take an arrival of each
+  // softmax warp.  With two dP tiles the softmax may be done with tile n + 1
+  // before the tensor core's warp has looked for tile n, so dp_full and
+  // ds_full alternate too: no barrier passes two phases unseen.
+  static constexpr int kNumBars = 2 + 2 * (kStagesA + kStagesB) + 8;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;   // tmem addr, abort flag
   static constexpr int kOffList = kOffMisc + 16;            // visited tiles, masked tiles: bits
   static constexpr int kSmemBytes = kOffList + 2 * kBwdMaxListed / 8;
@@ -104,30 +106,78 @@ struct BwdCfg {
   static constexpr uint32_t kIdescAcc = idesc_bf16_f32(128, D, 0, 1);
 };
 
+// A product's tcgen05.mma in one block, called by all lanes of a converged
+// warp: one election, the first shared-memory descriptors, and fixed steps of
+// their low words (16-byte units).  An election and a descriptor built from
+// its address for every instruction made the issuing warp the slowest part:
+// 60 - 120 cycles an instruction where N = 64 computes in 32.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // as smem_desc_sw128
+__device__ __forceinline__ uint32_t bwd_desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+
+// D[128 x 128] (+)= A[128 x 64] B[128 x 64]^T, both K-major blocks in shared memory.
+__device__ __forceinline__ void bwd_mma_ss4(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b32 a, b;\n\t.reg .b64 da, db;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t"
+      "setp.eq.b32 p, 0, 0;\n\t"
+      "add.u32 a, %1, 2;\n\tadd.u32 b, %2, 2;\n\t"
+      "mov.b64 da, {a, %5};\n\tmov.b64 db, {b, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t"
+      "add.u32 a, %1, 4;\n\tadd.u32 b, %2, 4;\n\t"
+      "mov.b64 da, {a, %5};\n\tmov.b64 db, {b, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t"
+      "add.u32 a, %1, 6;\n\tadd.u32 b, %2, 6;\n\t"
+      "mov.b64 da, {a, %5};\n\tmov.b64 db, {b, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
+      : "memory");
+}
+
 // D[128 x 128] = A[128 x D] B[128 x D]^T, both K-major tiles in shared memory.
 template <int D>
 __device__ __forceinline__ void bwd_issue_score(uint32_t d_tmem, uint32_t sA, uint32_t sB) {
   using C = BwdCfg<D>;
 #pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk) {
-    const uint32_t off = (kk / 4) * C::kSubBytes + (kk % 4) * 32;
-    mma_ss_elect(d_tmem, smem_desc_sw128(sA + off, 16, 1024), smem_desc_sw128(sB + off, 16, 1024),
-                 C::kIdescS, kk > 0 ? 1u : 0u);
-  }
+  for (int k = 0; k < C::kSub; ++k)
+    bwd_mma_ss4(d_tmem, bwd_desc_lo(sA, 16) + k * (C::kSubBytes >> 4),
+                bwd_desc_lo(sB, 16) + k * (C::kSubBytes >> 4), C::kIdescS, k > 0 ? 1u : 0u);
 }
 
-// Acc[128 x D] += A[128 x 128] B[128 x D]: A bf16 in tensor memory, 32 values
-// of a row in 16 columns, the next 32 from 32 columns on; B a shared tile.
+// Acc[128 x D] (+)= A[128 x 64] B[64 x D]: A bf16 in tensor memory, 32 values
+// of a row in 16 columns, the next 32 from 32 columns on; B 64 rows of a
+// shared tile (steps of 16 rows: 2048 bytes).
+__device__ __forceinline__ void bwd_mma_ts4(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b32 a, b;\n\t.reg .b64 db;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t"
+      "setp.eq.b32 p, 0, 0;\n\t"
+      "add.u32 a, %1, 8;\n\tadd.u32 b, %2, 128;\n\tmov.b64 db, {b, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+      "add.u32 a, %1, 32;\n\tadd.u32 b, %2, 256;\n\tmov.b64 db, {b, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t"
+      "add.u32 a, %1, 40;\n\tadd.u32 b, %2, 384;\n\tmov.b64 db, {b, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], db, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
+      : "memory");
+}
+// Acc[128 x D] += A[128 x 128] B[128 x D].
 template <int D>
 __device__ __forceinline__ void bwd_issue_acc(uint32_t d_tmem, uint32_t a_tmem, uint32_t sB,
                                               bool accumulate) {
   using C = BwdCfg<D>;
-#pragma unroll
-  for (int kk = 0; kk < 8; ++kk) {
-    const uint64_t b = smem_desc_sw128(sB + kk * 2048, C::kSubBytes, 1024);
-    mma_ts_elect(d_tmem, a_tmem + (kk / 2) * 32 + (kk % 2) * 8, b, C::kIdescAcc,
-                 (accumulate || kk > 0) ? 1u : 0u);
-  }
+  const uint32_t b = bwd_desc_lo(sB, C::kSubBytes);
+  bwd_mma_ts4(d_tmem, a_tmem, b, C::kIdescAcc, accumulate ? 1u : 0u);
+  bwd_mma_ts4(d_tmem, a_tmem + 64, b + 512, C::kIdescAcc, 1u);
 }
 
 // warp_wait_phase with its polling loop out of line: the phase has often
@@ -140,6 +190,23 @@ __device__ __forceinline__ bool bwd_wait(uint32_t bar, uint32_t parity, volatile
                                          int* err) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return bwd_wait_slow(bar, parity, abort_flag, err);
+}
+
+// Two or three phases at once: their first looks overlap.
+__device__ __forceinline__ bool bwd_wait2(uint32_t bar0, uint32_t par0, uint32_t bar1,
+                                          uint32_t par1, volatile int* abort_flag, int* err) {
+  const bool a = mbar_try_wait(bar0, par0), b = mbar_try_wait(bar1, par1);
+  if (__all_sync(0xffffffffu, a && b)) return true;
+  return bwd_wait_slow(bar0, par0, abort_flag, err) && bwd_wait_slow(bar1, par1, abort_flag, err);
+}
+__device__ __forceinline__ bool bwd_wait3(uint32_t bar0, uint32_t par0, uint32_t bar1,
+                                          uint32_t par1, uint32_t bar2, uint32_t par2,
+                                          volatile int* abort_flag, int* err) {
+  const bool a = mbar_try_wait(bar0, par0), b = mbar_try_wait(bar1, par1),
+             c = mbar_try_wait(bar2, par2);
+  if (__all_sync(0xffffffffu, a && b && c)) return true;
+  return bwd_wait_slow(bar0, par0, abort_flag, err) &&
+         bwd_wait_slow(bar1, par1, abort_flag, err) && bwd_wait_slow(bar2, par2, abort_flag, err);
 }
 
 // Untiled bulk copy into shared memory (16-byte aligned, size a multiple of 16).
@@ -313,8 +380,9 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
   auto b_par = [](int n) { return uint32_t(n / kB) & 1u; };
   constexpr int kX = C::dp_tiles(kKV);
   const uint32_t s_full = bar(kBars), done = bar(kBars + 3), s_free = bar(kBars + 4),
-                 p_full = bar(kBars + 5), ds_full = bar(kBars + 6);
+                 p_full = bar(kBars + 5);
   auto dp_full = [&](int n) { return bar(kBars + 1 + n % kX); };
+  auto ds_full = [&](int n) { return bar(kBars + 6 + n % kX); };
   auto dp_par = [](int n) { return uint32_t(n / kX) & 1u; };
   const uint32_t sFix[2] = {sbase + C::kOffFixed, sbase + C::kOffFixed + C::kTileBytes};
   auto sA = [&](int n) { return sbase + C::kOffRingA + (n % kA) * C::kTileBytes; };
@@ -448,46 +516,56 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
     auto wait = [&](uint32_t b_, uint32_t parity) {
       return bwd_wait(b_, parity, abort_flag, p.err);
     };
-    // scores of tile n, dP of tile n
+    // scores of tile n, dP of tile n (their tiles have landed)
     auto scores = [&](int n) {
-      if (!wait(a_full(n), a_par(n))) return false;
       tc_fence_after();
       bwd_issue_score<D>(tmem + C::tmem_s(kKV), sFix[0], sA(n));
       mma_commit_elect(s_full);
-      return true;
     };
     auto dprobs = [&](int n) {
-      if (!wait(b_full(n), b_par(n))) return false;
       tc_fence_after();
       bwd_issue_score<D>(tmem + C::tmem_dp(kKV, n), sFix[1], sB(n));
       mma_commit_elect(dp_full(n));
       if (!kKV) mma_commit_elect(b_empty(n));
-      return true;
     };
     bool ok = true;
-    if (n_tiles > 0) ok = wait(fixed_full(0), 0) && scores(0) && wait(fixed_full(1), 0) && dprobs(0);
+    if (n_tiles > 0) {
+      ok = wait(fixed_full(0), 0) && wait(a_full(0), 0);
+      if (ok) scores(0);
+      ok = ok && wait(fixed_full(1), 0) && wait(b_full(0), 0);
+      if (ok) dprobs(0);
+    }
     for (int n = 0; n < n_tiles && ok; ++n) {
       const bool more = n + 1 < n_tiles;
       const uint32_t tp = uint32_t(n) & 1u;
       const uint32_t tX = tmem + C::tmem_dp(kKV, n);
-      // the next scores once these are in registers, and, into the other dP
-      // tile (whose P and dS the products of tile n - 1 have read), the next dP
-      if (more) ok = wait(s_free, tp) && scores(n + 1);
-      if (more && kX == 2) ok = ok && dprobs(n + 1);
+      if (more) {
+        // the next scores once these are in registers, and, into the other dP
+        // tile (whose P and dS the products of tile n - 1 have read), the next
+        // dP
+        ok = kX == 2 ? bwd_wait3(s_free, tp, a_full(n + 1), a_par(n + 1), b_full(n + 1),
+                                 b_par(n + 1), abort_flag, p.err)
+                     : bwd_wait2(s_free, tp, a_full(n + 1), a_par(n + 1), abort_flag, p.err);
+        if (!ok) break;
+        scores(n + 1);
+        if (kX == 2) dprobs(n + 1);
+      }
       if (kKV && kX == 1) {   // P is ready before dS
-        ok = ok && wait(p_full, tp);
+        ok = wait(p_full, tp);
         if (!ok) break;
         tc_fence_after();
         bwd_issue_acc<D>(tmem + C::kTmemAcc0, tX, sB(n), n > 0);
       }
-      ok = ok && wait(ds_full, tp);
+      ok = more && kX == 1 ? bwd_wait2(ds_full(n), dp_par(n), b_full(n + 1), b_par(n + 1),
+                                       abort_flag, p.err)
+                           : wait(ds_full(n), dp_par(n));
       if (!ok) break;
       tc_fence_after();
       if (kKV && kX == 2) bwd_issue_acc<D>(tmem + C::kTmemAcc0, tX, sB(n), n > 0);
       bwd_issue_acc<D>(tmem + (kKV ? C::kTmemAcc1 : C::kTmemAcc0), tX + 16, sA(n), n > 0);
       mma_commit_elect(a_empty(n));
       if (kKV) mma_commit_elect(b_empty(n));   // the statistics were read before ds_full
-      if (more && kX == 1) ok = dprobs(n + 1);   // over P and dS
+      if (more && kX == 1) dprobs(n + 1);   // over P and dS
     }
     // every product issued has finished before the epilogue and the release
     // of tensor memory
@@ -549,9 +627,10 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
       const float* stats =
           reinterpret_cast<const float*>(smem + C::kOffStats + (n % kB) * C::kStatBytes) + x0;
       // the statistics of this query tile, then its scores
-      if (kKV) ok = wait(b_full(n), b_par(n));
-      ok = ok && wait(s_full, uint32_t(n) & 1u);
+      ok = kKV ? bwd_wait2(b_full(n), b_par(n), s_full, uint32_t(n) & 1u, abort_flag, p.err)
+               : bwd_wait(s_full, uint32_t(n) & 1u, abort_flag, p.err);
       if (!ok) break;
+      tc_fence_after();
       uint32_t rr[32], pk[16];
       float pr[32];
       tmem_ld32(tS, rr);
@@ -580,7 +659,7 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
       bwd_dscores32<kKV>(rr, ndelta, stats + 128, pr, pk);
       tmem_st16(tX + 16, pk);
       tmem_st_wait();
-      arrive(ds_full);
+      arrive(ds_full(n));
     }
     // ------------------------------------------------------------ epilogue
     ok = ok && warp_wait_phase(done, 0, abort_flag, p.err);
