@@ -17,12 +17,11 @@ namespace vidattn {
 namespace {
 
 constexpr int kBwdMaxSplit = 64;
-constexpr int kBwdEmu = 4;   // exponentials of 16 on the FMA pipe
 
 using BwdKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap,
                            const CUtensorMap, const BwdParams);
 BwdKernel bwd_variant(int D) {
-  return D == 128 ? vidattn_bwd_kernel<128, kBwdEmu> : vidattn_bwd_kernel<64, kBwdEmu>;
+  return D == 128 ? vidattn_bwd_kernel<128> : vidattn_bwd_kernel<64>;
 }
 int bwd_smem(int D) { return D == 128 ? BwdCfg<128>::kSmemBytes : BwdCfg<64>::kSmemBytes; }
 

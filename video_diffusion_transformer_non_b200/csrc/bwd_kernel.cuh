@@ -274,9 +274,11 @@ static __device__ __noinline__ uint32_t bwd_mask32(int x0, int lo, int hi, const
 }
 
 // 32 scores of a row (r) to probabilities: 2^(c s + off), off the row's
-// (kPerColumn false) or read per column from shared memory.  Of every 16, the
-// last kEmu on the FMA pipe.
-template <int kEmu, bool kPerColumn>
+// (kPerColumn false) or read per column from shared memory.  All on the
+// special-function unit: a share of them as a polynomial on the FMA pipe costs
+// issue slots here (D = 128, 8192 tokens: 693 us with 4 of 16, 671 with 2, 662
+// with none; D = 64: 510, 498, 488).
+template <bool kPerColumn>
 __device__ __forceinline__ void bwd_probs32(const uint32_t (&r)[32], float c, float off,
                                             const float* offs, float (&pr)[32]) {
   const float2 c2 = make_float2(c, c);
@@ -289,15 +291,8 @@ __device__ __forceinline__ void bwd_probs32(const uint32_t (&r)[32], float c, fl
       const int e = x + y;
       const float2 arg = ffma2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), c2,
                                y == 0 ? make_float2(o.x, o.y) : make_float2(o.z, o.w));
-      float2 v;
-      if ((e & 15) < 16 - kEmu) {
-        v.x = ex2(arg.x);
-        v.y = ex2(arg.y);
-      } else {
-        v = exp2_poly2(arg);
-      }
-      pr[e] = v.x;
-      pr[e + 1] = v.y;
+      pr[e] = ex2(arg.x);
+      pr[e + 1] = ex2(arg.y);
     }
   }
 }
@@ -358,7 +353,7 @@ __device__ __forceinline__ void bwd_store_row(uint32_t taddr, bool have, bool ro
 }
 
 // One unit.  kKV: it owns key tile `own`; else query tile `own`.
-template <int D, int kEmu, bool kKV>
+template <int D, bool kKV>
 __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                          const CUtensorMap& tm_v, const CUtensorMap& tm_do,
                                          const BwdParams& p, uint32_t sbase, uint8_t* smem,
@@ -637,7 +632,7 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
       tmem_ld_wait();
       reg_fence(rr);
       arrive(s_free);
-      bwd_probs32<kEmu, kKV>(rr, p.c, nlse, stats, pr);
+      bwd_probs32<kKV>(rr, p.c, nlse, stats, pr);
       if (masked) {
 #pragma unroll
         for (int x = 0; x < 32; ++x) pr[x] = (vis >> x) & 1 ? pr[x] : 0.f;
@@ -690,7 +685,7 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
 // first, each kind with the split fastest, then the tile, then (b, h): the
 // units of one head run close together and share its tiles in L2.  With the
 // causal limit the longest tiles of a head go first.
-template <int D, int kEmu>
+template <int D>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     vidattn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k,
@@ -731,14 +726,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   if (u < p.n_kv_units) {
     const int split = u % p.n_kv_split;
     u /= p.n_kv_split;
-    bwd_unit<D, kEmu, true>(tm_q, tm_k, tm_v, tm_do, p, sbase, smem, tmem, u / p.n_kv_tiles,
+    bwd_unit<D, true>(tm_q, tm_k, tm_v, tm_do, p, sbase, smem, tmem, u / p.n_kv_tiles,
                             u % p.n_kv_tiles, split, p.n_kv_split);
   } else {
     u -= p.n_kv_units;
     const int split = u % p.n_q_split;
     u /= p.n_q_split;
     const int t = u % p.n_q_tiles;
-    bwd_unit<D, kEmu, false>(tm_q, tm_k, tm_v, tm_do, p, sbase, smem, tmem, u / p.n_q_tiles,
+    bwd_unit<D, false>(tm_q, tm_k, tm_v, tm_do, p, sbase, smem, tmem, u / p.n_q_tiles,
                              p.causal ? p.n_q_tiles - 1 - t : t, split, p.n_q_split);
   }
 
