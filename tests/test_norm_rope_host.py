@@ -76,7 +76,7 @@ def test_norm_workspace():
     ws = binding.layernorm_bwd_workspace
     assert ws(1, 1, 1, 64, 0) == 512
     assert ws(1, 1, 10 ** 6, 128, 0) == 148 * 8 * 2 * 128 * 4
-    assert ws(1, 1, 1000, 5120, 1) == 148 * (2048 // 640) * 2 * 5120 * 4
+    assert ws(1, 1, 1000, 5120, 1) == 148 * (2048 // 320) * 2 * 5120 * 4
     assert ws(1, 1, 0, 64, 0) == 0
     assert ws(0, 1, 1, 64, 0) == -1 and ws(1, 1, 1, 64, 5) == -1 and ws(1, 1, 1, 20000, 0) == -1
 

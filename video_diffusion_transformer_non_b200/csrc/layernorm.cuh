@@ -11,12 +11,14 @@
 // rows stay in its registers until the end; the CTAs' partial sums go to the
 // workspace and are added by a second kernel in a fixed order.
 //
-// Rows of up to 1024 features belong to 8, 16 or 32 lanes of a warp, several
-// rows in flight a thread (no barrier); longer ones to a CTA of ceil(N / 8)
-// threads, the next rows' loads in flight while the present ones are reduced.
-// Rows that lie on 16-byte boundaries with N a multiple of 8 move in 16-byte
-// loads (8 neighbouring features a thread); any other N or stride takes the
-// same code with single features, neighbouring lanes on neighbouring ones.
+// Rows of up to 1024 features belong to 8, 16 or 32 lanes of a warp (no
+// barrier); longer ones to a CTA with 16 features a thread.  What bounds the pass
+// is how many bytes are in flight: rows that lie on 16-byte boundaries with N
+// a multiple of 8 go through a ring in shared memory, filled by cp.async up to
+// three turns ahead, each thread copying and reading its own 8 neighbouring
+// features (so the ring needs no barrier).  Any other N or stride takes the
+// same code with single features, neighbouring lanes on neighbouring ones, and
+// the next rows in registers.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -29,9 +31,11 @@ namespace vidattn {
 constexpr int kLnMaxN = 16384;
 constexpr int kLnThreads = 256;   // of the kernels with several rows a CTA
 
-// Rows of a logical [B,H,S,N] array: strides in elements.
+// Rows of a logical [B,H,S,N] array: strides in elements; flat: row r of all
+// B * H * S lies at r * ss (below 2^31).
 struct LnLayout {
   long long sb, sh, ss;
+  int flat;
 };
 
 struct LnParams {
@@ -43,12 +47,14 @@ struct LnParams {
   int rows, N;
   FastDiv div_s, div_h;
   int params_bf16;
-  float eps;
+  float eps, inv_n;
 };
 
-__device__ __forceinline__ long long ln_offset(const LnParams& p, const LnLayout& l, int row) {
-  const uint32_t bh = fastdiv(uint32_t(row), p.div_s);
-  const uint32_t s = uint32_t(row) - bh * p.div_s.d;
+__device__ __forceinline__ long long ln_offset(const LnParams& p, const LnLayout& l,
+                                               uint32_t row) {
+  if (l.flat) return (long long)(uint64_t(row) * uint32_t(l.ss));
+  const uint32_t bh = fastdiv(row, p.div_s);
+  const uint32_t s = row - bh * p.div_s.d;
   const uint32_t b = fastdiv(bh, p.div_h);
   const uint32_t h = bh - b * p.div_h.d;
   return b * l.sb + h * l.sh + s * l.ss;
@@ -57,6 +63,23 @@ __device__ __forceinline__ long long ln_offset(const LnParams& p, const LnLayout
 __device__ __forceinline__ float ln_bf16(uint16_t v) { return __uint_as_float(uint32_t(v) << 16); }
 __device__ __forceinline__ uint16_t ln_to_bf16(float v) {
   return static_cast<uint16_t>(pack_bf16x2(v, v) & 0xffffu);
+}
+
+// Turns of the ring: up to 4 in 192 KB, or in 64 KB where several CTAs fit an SM
+// (fewer than 2: rows go through registers).
+__host__ __device__ constexpr int ln_stages(int threads, int rows, int tensors, int bytes_a_thread) {
+  const int stage = threads * rows * tensors * bytes_a_thread;
+  int n = (threads <= 512 ? 65536 : 196608) / stage;
+  if (n < 2 && 2 * stage <= 196608) n = 2;
+  return n > 4 ? 4 : n;
+}
+__device__ __forceinline__ void ln_copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void ln_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void ln_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
 // kC chunks of 8 features of one row, as read: X is float or uint16_t (bf16).
@@ -103,32 +126,61 @@ struct LnFrag {
       }
     }
   }
-  __device__ __forceinline__ float get(int e) const {
+  // The same by way of shared memory: kPieces pieces of 16 bytes a thread, at
+  // `ring` (a shared address of this thread's) and every `pitch` bytes from
+  // there.  valid: which chunks begin in front of N.
+  static constexpr int kPieces = kWords / 4;
+  static __device__ __forceinline__ void copy(uint32_t ring, uint32_t pitch, const X* row,
+                                              int lane, int lanes, const bool (&valid)[kC]) {
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+      if (valid[c]) {
+#pragma unroll
+        for (int k = 0; k < kPieces / kC; ++k)
+          ln_copy16(ring + (c * (kPieces / kC) + k) * pitch,
+                    reinterpret_cast<const char*>(row + (c * lanes + lane) * 8) + 16 * k);
+      }
+    }
+  }
+  __device__ __forceinline__ void read(uint32_t ring, uint32_t pitch, const bool (&valid)[kC]) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      uint32_t* d = r + 4 * i;
+      d[0] = d[1] = d[2] = d[3] = 0u;
+      if (valid[i / (kPieces / kC)])
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+                     : "r"(ring + i * pitch)
+                     : "memory");
+    }
+  }
+  // Elements 2 i and 2 i + 1.
+  __device__ __forceinline__ float2 get2(int i) const {
     if constexpr (kVec && kBf16)
-      return __uint_as_float((e & 1) ? r[e >> 1] & 0xffff0000u : r[e >> 1] << 16);
+      return make_float2(__uint_as_float(r[i] << 16), __uint_as_float(r[i] & 0xffff0000u));
     else
-      return __uint_as_float(r[e]);
+      return make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
   }
 };
+__device__ __forceinline__ float2 ln_both(float v) { return make_float2(v, v); }
 
 template <typename X, int kC, bool kVec>
 __device__ __forceinline__ void ln_store(X* row, int lane, int lanes, int N,
-                                         const float (&v)[8 * kC]) {
+                                         const float2 (&v)[4 * kC]) {
   if constexpr (kVec) {
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
       const int at = (c * lanes + lane) * 8;
       if (at >= N) continue;
-      const float* s = v + 8 * c;
-      uint4* d = reinterpret_cast<uint4*>(row + at);
+      const float2* s = v + 4 * c;
       if constexpr (sizeof(X) == 2) {
-        *d = make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]),
-                        pack_bf16x2(s[6], s[7]));
+        *reinterpret_cast<uint4*>(row + at) =
+            make_uint4(pack_bf16x2(s[0].x, s[0].y), pack_bf16x2(s[1].x, s[1].y),
+                       pack_bf16x2(s[2].x, s[2].y), pack_bf16x2(s[3].x, s[3].y));
       } else {
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          d[k] = make_uint4(__float_as_uint(s[4 * k]), __float_as_uint(s[4 * k + 1]),
-                            __float_as_uint(s[4 * k + 2]), __float_as_uint(s[4 * k + 3]));
+        float4* d = reinterpret_cast<float4*>(row + at);
+        d[0] = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
+        d[1] = make_float4(s[2].x, s[2].y, s[3].x, s[3].y);
       }
     }
   } else {
@@ -136,24 +188,40 @@ __device__ __forceinline__ void ln_store(X* row, int lane, int lanes, int N,
     for (int e = 0; e < 8 * kC; ++e) {
       const int at = e * lanes + lane;
       if (at < N) {
-        if constexpr (sizeof(X) == 2) row[at] = ln_to_bf16(v[e]);
-        else row[at] = v[e];
+        const float t = (e & 1) ? v[e / 2].y : v[e / 2].x;
+        if constexpr (sizeof(X) == 2) row[at] = ln_to_bf16(t);
+        else row[at] = t;
       }
     }
   }
 }
 
 // This thread's features of weight or bias (null: `none`).
-template <int kC, bool kVec>
-__device__ __forceinline__ void ln_params(const void* src, int bf16, int lane, int lanes, int N,
-                                          float none, float (&v)[8 * kC]) {
+template <typename P, int kC, bool kVec>
+__device__ __forceinline__ void ln_params_of(const P* src, int lane, int lanes, int N,
+                                             float2 (&v)[4 * kC]) {
+  P t[8 * kC];
 #pragma unroll
   for (int e = 0; e < 8 * kC; ++e) {
     const int at = LnFrag<float, kC, kVec>::col(e, lane, lanes);
-    v[e] = none;
-    if (src != nullptr && at < N)
-      v[e] = bf16 ? ln_bf16(__ldg(static_cast<const uint16_t*>(src) + at))
-                  : __ldg(static_cast<const float*>(src) + at);
+    t[e] = at < N ? __ldg(src + at) : P(0);
+  }
+#pragma unroll
+  for (int e = 0; e < 4 * kC; ++e) {
+    if constexpr (sizeof(P) == 2) v[e] = make_float2(ln_bf16(t[2 * e]), ln_bf16(t[2 * e + 1]));
+    else v[e] = make_float2(t[2 * e], t[2 * e + 1]);
+  }
+}
+template <int kC, bool kVec>
+__device__ __forceinline__ void ln_params(const void* src, int bf16, int lane, int lanes, int N,
+                                          float none, float2 (&v)[4 * kC]) {
+  if (src == nullptr) {
+#pragma unroll
+    for (int e = 0; e < 4 * kC; ++e) v[e] = ln_both(none);
+  } else if (bf16) {
+    ln_params_of<uint16_t, kC, kVec>(static_cast<const uint16_t*>(src), lane, lanes, N, v);
+  } else {
+    ln_params_of<float, kC, kVec>(static_cast<const float*>(src), lane, lanes, N, v);
   }
 }
 
@@ -176,192 +244,310 @@ __device__ __forceinline__ void ln_sum(float (&v)[kN], int lanes, float (*buf)[3
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      v[i] = lane < n ? buf[i][lane] : 0.f;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    for (int i = 0; i < kN; ++i) {   // every thread adds the warps' sums, in order
+      float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < n; w += 4) {   // buf is zero behind the last warp
+        const float4 u = *reinterpret_cast<const float4*>(&buf[i][w]);
+        t.x += u.x, t.y += u.y, t.z += u.z, t.w += u.w;
+      }
+      v[i] = (t.x + t.y) + (t.z + t.w);
     }
   }
 }
 
-// The rows a thread works on: kR at a time.  kBlock: the CTA's kR next rows;
-// else every group of kLanes threads has a row of its own in each of kR turns.
-template <typename X, int kLanes, int kC, int kR, bool kVec, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads) ln_fwd_kernel(const LnParams p) {
-  constexpr bool kBlock = kLanes == 0;
-  constexpr int kE = 8 * kC;
+extern __shared__ uint4 ln_ring[];
+
+// What both kernels share: the rows a thread works on, kR at a time (kBlock:
+// the CTA's kR next rows; else every group of kLanes threads has a row of its
+// own in each of kR turns), its features, and the ring.
+template <typename X, int kLanes, int kC, int kR, bool kVec, int kMaxThreads, int kTensors>
+struct LnWalk {
+  static constexpr bool kBlock = kLanes == 0;
   using Frag = LnFrag<X, kC, kVec>;
-  __shared__ float buf[kBlock ? 4 : 1][kR][32];
-  const int lanes = kBlock ? blockDim.x : kLanes;
-  const int lane = kBlock ? threadIdx.x : threadIdx.x % (kBlock ? 1 : kLanes);
-  const int group = kBlock ? 0 : threadIdx.x / (kBlock ? 1 : kLanes);
-  const int groups = kBlock ? 1 : kLnThreads / (kBlock ? 1 : kLanes);
+  static constexpr int kS = kVec ? ln_stages(kMaxThreads, kR, kTensors, Frag::kWords * 4) : 0;
+  static constexpr bool kRing = kS >= 2;
+  int lanes, lane, groups, group;
+  uint32_t row, step, pitch, stage, ring, in, out;   // in, out: ring addresses of this thread's
+  bool valid[kC];
+  __device__ __forceinline__ explicit LnWalk(const LnParams& p) {
+    lanes = kBlock ? blockDim.x : kLanes;
+    lane = kBlock ? threadIdx.x : threadIdx.x % (kBlock ? 1 : kLanes);
+    group = kBlock ? 0 : threadIdx.x / (kBlock ? 1 : kLanes);
+    groups = kBlock ? 1 : kLnThreads / (kBlock ? 1 : kLanes);
+    row = blockIdx.x * groups * kR + group;
+    step = gridDim.x * groups * kR;
+    pitch = blockDim.x * 16;
+    stage = pitch * Frag::kWords / 4 * kTensors * kR;
+    ring = smem_u32(ln_ring) + threadIdx.x * 16;
+    in = out = ring;
+#pragma unroll
+    for (int c = 0; c < kC; ++c) valid[c] = (c * lanes + lane) * 8 < p.N;
+  }
+  // the CTA's first row of this turn decides whether the turn is made at all
+  __device__ __forceinline__ bool any(const LnParams& p) const { return row - group < p.rows; }
+  __device__ __forceinline__ uint32_t slot(uint32_t at, int i, int tensor) const {
+    return at + (i * kTensors + tensor) * (Frag::kWords / 4) * pitch;
+  }
+  __device__ __forceinline__ void next(uint32_t& at) const {
+    at += stage;
+    if (at == ring + kS * stage) at = ring;
+  }
+};
+
+template <typename X, int kLanes, int kC, int kR, bool kVec, int kMaxThreads, int kCtas>
+__global__ void __launch_bounds__(kMaxThreads, kCtas) ln_fwd_kernel(const LnParams p) {
+  using Walk = LnWalk<X, kLanes, kC, kR, kVec, kMaxThreads, 1>;
+  using Frag = typename Walk::Frag;
+  constexpr bool kBlock = Walk::kBlock, kRing = Walk::kRing;
+  constexpr int kE = 8 * kC, kS = Walk::kS;
+  __shared__ __align__(16) float buf[kBlock ? 4 : 1][kR][32];
+  if (kBlock) {
+    for (int i = threadIdx.x; i < 4 * kR * 32; i += blockDim.x) (&buf[0][0][0])[i] = 0.f;
+    __syncthreads();
+  }
+  Walk t(p);
+  const int lane = t.lane, lanes = t.lanes;
   const X* x = static_cast<const X*>(p.x);
   X* y = static_cast<X*>(p.y);
-  float w[kE], b[kE];
-  ln_params<kC, kVec>(p.w, p.params_bf16, lane, lanes, p.N, 1.f, w);
-  ln_params<kC, kVec>(p.b, p.params_bf16, lane, lanes, p.N, 0.f, b);
-  const float n = float(p.N);
-  const int64_t step = int64_t(gridDim.x) * groups * kR;
-  int turn = 0;
-
-  Frag next[kR];
-  auto fetch = [&](int64_t base) {
+  Frag next[kRing ? 1 : kR];
+  auto fetch = [&](uint32_t row0) {
 #pragma unroll
     for (int i = 0; i < kR; ++i) {
-      const int64_t row = base + int64_t(i) * groups + group;
-      if (row < p.rows) next[i].load(x + ln_offset(p, p.lx, int(row)), lane, lanes, p.N);
-      else next[i].clear();
+      const uint32_t row = row0 + i * t.groups;
+      if constexpr (kRing) {
+        if (row < p.rows)
+          Frag::copy(t.slot(t.in, i, 0), t.pitch, x + ln_offset(p, p.lx, row), lane, lanes,
+                     t.valid);
+      } else {
+        if (row < p.rows) next[i].load(x + ln_offset(p, p.lx, row), lane, lanes, p.N);
+        else next[i].clear();
+      }
+    }
+    if constexpr (kRing) {
+      t.next(t.in);
+      ln_commit();
     }
   };
-  int64_t base = int64_t(blockIdx.x) * groups * kR;
-  if (base < p.rows) fetch(base);
-  for (; base < p.rows; base += step, turn ^= 1) {
-    Frag cur[kR];
+  if constexpr (kRing) {
 #pragma unroll
-    for (int i = 0; i < kR; ++i) cur[i] = next[i];
-    if (kBlock && base + step < p.rows) fetch(base + step);
+    for (int k = 0; k < kS - 1; ++k) fetch(t.row + k * t.step);
+  } else {
+    fetch(t.row);
+  }
+  float2 w[kE / 2], b[kE / 2];
+  ln_params<kC, kVec>(p.w, p.params_bf16, lane, lanes, p.N, 1.f, w);
+  ln_params<kC, kVec>(p.b, p.params_bf16, lane, lanes, p.N, 0.f, b);
+  for (int turn = 0; t.any(p); turn ^= 1, t.row += t.step) {
+    Frag cur[kR];
+    if constexpr (kRing) {
+      fetch(t.row + (kS - 1) * t.step);
+      ln_wait<kRing ? kS - 1 : 0>();
+#pragma unroll
+      for (int i = 0; i < kR; ++i) cur[i].read(t.slot(t.out, i, 0), t.pitch, t.valid);
+      t.next(t.out);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kR; ++i) cur[i] = next[i];
+      if (kBlock) fetch(t.row + t.step);
+    }
     float mean[kR], var[kR];
+    float2 d[kR][kE / 2];
 #pragma unroll
     for (int i = 0; i < kR; ++i) {
-      mean[i] = 0.f;
+      float2 s = ln_both(0.f);
 #pragma unroll
-      for (int e = 0; e < kE; ++e) mean[i] += cur[i].get(e);
+      for (int e = 0; e < kE / 2; ++e) {
+        d[i][e] = cur[i].get2(e);
+        s = fadd2(s, d[i][e]);
+      }
+      mean[i] = s.x + s.y;
     }
     ln_sum<kBlock>(mean, lanes, buf[kBlock ? 2 * turn : 0]);
 #pragma unroll
     for (int i = 0; i < kR; ++i) {
-      mean[i] /= n;
-      var[i] = 0.f;
+      mean[i] *= p.inv_n;
+      float2 s = ln_both(0.f);
 #pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        const float d = cur[i].get(e) - mean[i];
-        if (Frag::col(e, lane, lanes) < p.N) var[i] = fmaf(d, d, var[i]);
+      for (int e = 0; e < kE / 2; ++e) {
+        d[i][e] = fadd2(d[i][e], ln_both(-mean[i]));
+        if (kVec) {   // features behind N add nothing
+          if (t.valid[e / 4]) s = ffma2(d[i][e], d[i][e], s);
+        } else {
+          if (Frag::col(2 * e, lane, lanes) < p.N) s.x = fmaf(d[i][e].x, d[i][e].x, s.x);
+          if (Frag::col(2 * e + 1, lane, lanes) < p.N) s.y = fmaf(d[i][e].y, d[i][e].y, s.y);
+        }
       }
+      var[i] = s.x + s.y;
     }
     ln_sum<kBlock>(var, lanes, buf[kBlock ? 2 * turn + 1 : 0]);
 #pragma unroll
     for (int i = 0; i < kR; ++i) {
-      const int64_t row = base + int64_t(i) * groups + group;
-      const float rstd = 1.f / sqrtf(var[i] / n + p.eps);
+      const uint32_t row = t.row + i * t.groups;
+      const float rstd = rsqrtf(fmaf(var[i], p.inv_n, p.eps));
       if (row < p.rows) {
-        float v[kE];
 #pragma unroll
-        for (int e = 0; e < kE; ++e) v[e] = fmaf((cur[i].get(e) - mean[i]) * rstd, w[e], b[e]);
-        ln_store<X, kC, kVec>(y + ln_offset(p, p.ly, int(row)), lane, lanes, p.N, v);
+        for (int e = 0; e < kE / 2; ++e) d[i][e] = ffma2(fmul2(d[i][e], ln_both(rstd)), w[e], b[e]);
+        ln_store<X, kC, kVec>(y + ln_offset(p, p.ly, row), lane, lanes, p.N, d[i]);
         if (lane == 0) {
           if (p.mean) p.mean[row] = mean[i];
           if (p.rstd) p.rstd[row] = rstd;
         }
       }
     }
-    if (!kBlock && base + step < p.rows) fetch(base + step);
+    if (!kRing && !kBlock) fetch(t.row + t.step);
   }
 }
 
-template <typename X, int kLanes, int kC, int kR, bool kVec, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads) ln_bwd_kernel(const LnParams p) {
-  constexpr bool kBlock = kLanes == 0;
-  constexpr int kE = 8 * kC;
-  using Frag = LnFrag<X, kC, kVec>;
-  __shared__ float buf[kBlock ? 2 : 1][2 * kR][32];
+template <typename X, int kLanes, int kC, int kR, bool kVec, int kMaxThreads, int kCtas>
+__global__ void __launch_bounds__(kMaxThreads, kCtas) ln_bwd_kernel(const LnParams p) {
+  using Walk = LnWalk<X, kLanes, kC, kR, kVec, kMaxThreads, 2>;
+  using Frag = typename Walk::Frag;
+  constexpr bool kBlock = Walk::kBlock, kRing = Walk::kRing;
+  constexpr int kE = 8 * kC, kS = Walk::kS;
+  // xh and g are kept from the sums to the result where registers allow
+  constexpr bool kKeep = kE * kR <= 16 && kMaxThreads <= 320;
+  __shared__ __align__(16) float buf[kBlock ? 2 : 1][2 * kR][32];
+  if (kBlock) {
+    for (int i = threadIdx.x; i < 4 * kR * 32; i += blockDim.x) (&buf[0][0][0])[i] = 0.f;
+    __syncthreads();
+  }
   // one row of partial sums of every warp
   __shared__ float sums[kBlock ? 1 : kLnThreads / 32][kBlock ? 1 : (kBlock ? 1 : kLanes) * kE];
-  const int lanes = kBlock ? blockDim.x : kLanes;
-  const int lane = kBlock ? threadIdx.x : threadIdx.x % (kBlock ? 1 : kLanes);
-  const int group = kBlock ? 0 : threadIdx.x / (kBlock ? 1 : kLanes);
-  const int groups = kBlock ? 1 : kLnThreads / (kBlock ? 1 : kLanes);
+  Walk t(p);
+  const int lane = t.lane, lanes = t.lanes;
   const X* x = static_cast<const X*>(p.x);
   const X* dy = static_cast<const X*>(p.dy);
   X* dx = static_cast<X*>(p.y);
-  float w[kE], dw[kE], db[kE];
-  ln_params<kC, kVec>(p.w, p.params_bf16, lane, lanes, p.N, 1.f, w);
+  float2 w[kE / 2], dw[kE / 2], db[kE / 2];
 #pragma unroll
-  for (int e = 0; e < kE; ++e) dw[e] = db[e] = 0.f;
-  const float n = float(p.N);
-  const int64_t step = int64_t(gridDim.x) * groups * kR;
-  int turn = 0;
-
-  Frag nx[kR], ng[kR];
+  for (int e = 0; e < kE / 2; ++e) dw[e] = db[e] = ln_both(0.f);
+  Frag nx[kRing ? 1 : kR], ng[kRing ? 1 : kR];
   float nm[kR], nr[kR];
-  auto fetch = [&](int64_t base) {
+  auto fetch = [&](uint32_t row0) {
 #pragma unroll
     for (int i = 0; i < kR; ++i) {
-      const int64_t row = base + int64_t(i) * groups + group;
-      nm[i] = nr[i] = 0.f;
-      if (row < p.rows) {
-        nx[i].load(x + ln_offset(p, p.lx, int(row)), lane, lanes, p.N);
-        ng[i].load(dy + ln_offset(p, p.ldy, int(row)), lane, lanes, p.N);
-        nm[i] = __ldg(p.mean + row);
-        nr[i] = __ldg(p.rstd + row);
+      const uint32_t row = row0 + i * t.groups;
+      if constexpr (kRing) {
+        if (row < p.rows) {
+          Frag::copy(t.slot(t.in, i, 0), t.pitch, x + ln_offset(p, p.lx, row), lane, lanes,
+                     t.valid);
+          Frag::copy(t.slot(t.in, i, 1), t.pitch, dy + ln_offset(p, p.ldy, row), lane, lanes,
+                     t.valid);
+        }
+      } else if (row < p.rows) {
+        nx[i].load(x + ln_offset(p, p.lx, row), lane, lanes, p.N);
+        ng[i].load(dy + ln_offset(p, p.ldy, row), lane, lanes, p.N);
       } else {
         nx[i].clear();
         ng[i].clear();
       }
     }
+    if constexpr (kRing) {
+      t.next(t.in);
+      ln_commit();
+    }
   };
-  int64_t base = int64_t(blockIdx.x) * groups * kR;
-  if (base < p.rows) fetch(base);
-  for (; base < p.rows; base += step, turn ^= 1) {
+  auto fetch_stats = [&](uint32_t row0) {   // one turn ahead
+#pragma unroll
+    for (int i = 0; i < kR; ++i) {
+      const uint32_t row = row0 + i * t.groups;
+      nm[i] = nr[i] = 0.f;
+      if (row < p.rows) {
+        nm[i] = __ldg(p.mean + row);
+        nr[i] = __ldg(p.rstd + row);
+      }
+    }
+  };
+  fetch_stats(t.row);
+  if constexpr (kRing) {
+#pragma unroll
+    for (int k = 0; k < kS - 1; ++k) fetch(t.row + k * t.step);
+  } else {
+    fetch(t.row);
+  }
+  ln_params<kC, kVec>(p.w, p.params_bf16, lane, lanes, p.N, 1.f, w);
+  for (int turn = 0; t.any(p); turn ^= 1, t.row += t.step) {
     Frag cx[kR], cg[kR];
     float m[kR], r[kR], c[2 * kR];
 #pragma unroll
-    for (int i = 0; i < kR; ++i) cx[i] = nx[i], cg[i] = ng[i], m[i] = nm[i], r[i] = nr[i];
-    if (kBlock && base + step < p.rows) fetch(base + step);
+    for (int i = 0; i < kR; ++i) m[i] = -nm[i], r[i] = nr[i];
+    fetch_stats(t.row + t.step);
+    if constexpr (kRing) {
+      fetch(t.row + (kS - 1) * t.step);
+      ln_wait<kRing ? kS - 1 : 0>();
+#pragma unroll
+      for (int i = 0; i < kR; ++i) {
+        cx[i].read(t.slot(t.out, i, 0), t.pitch, t.valid);
+        cg[i].read(t.slot(t.out, i, 1), t.pitch, t.valid);
+        if (t.row + i * t.groups >= p.rows) cx[i].clear(), cg[i].clear();   // no row: no share
+      }
+      t.next(t.out);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kR; ++i) cx[i] = nx[i], cg[i] = ng[i];
+      if (kBlock) fetch(t.row + t.step);
+    }
+    float2 kx[kKeep ? kR : 1][kKeep ? kE / 2 : 1], kg[kKeep ? kR : 1][kKeep ? kE / 2 : 1];
 #pragma unroll
     for (int i = 0; i < kR; ++i) {
-      float c1 = 0.f, c2 = 0.f;
+      float2 c1 = ln_both(0.f), c2 = ln_both(0.f);
 #pragma unroll
-      for (int e = 0; e < kE; ++e) {   // dy is 0 behind N
-        const float xh = (cx[i].get(e) - m[i]) * r[i], g = cg[i].get(e);
-        const float gw = g * w[e];
-        c1 += gw;
-        c2 = fmaf(gw, xh, c2);
-        dw[e] = fmaf(g, xh, dw[e]);
-        db[e] += g;
+      for (int e = 0; e < kE / 2; ++e) {   // dy is 0 behind N
+        const float2 xh = fmul2(fadd2(cx[i].get2(e), ln_both(m[i])), ln_both(r[i]));
+        const float2 g = cg[i].get2(e), gw = fmul2(g, w[e]);
+        c1 = fadd2(c1, gw);
+        c2 = ffma2(gw, xh, c2);
+        dw[e] = ffma2(g, xh, dw[e]);
+        db[e] = fadd2(db[e], g);
+        if (kKeep) kx[kKeep ? i : 0][kKeep ? e : 0] = xh, kg[kKeep ? i : 0][kKeep ? e : 0] = gw;
       }
-      c[2 * i] = c1;
-      c[2 * i + 1] = c2;
+      c[2 * i] = c1.x + c1.y;
+      c[2 * i + 1] = c2.x + c2.y;
     }
     ln_sum<kBlock>(c, lanes, buf[kBlock ? turn : 0]);
 #pragma unroll
     for (int i = 0; i < kR; ++i) {
-      const int64_t row = base + int64_t(i) * groups + group;
-      if (row < p.rows) {
-        const float c1 = c[2 * i] / n, c2 = c[2 * i + 1] / n;
-        float v[kE];
+      const uint32_t row = t.row + i * t.groups;
+      if (row < p.rows) {   // dx = r g - r c1 - xh r c2
+        const float rn = -r[i] * p.inv_n;
+        const float2 c1 = ln_both(c[2 * i] * rn), c2 = ln_both(c[2 * i + 1] * rn);
+        float2 v[kE / 2];
 #pragma unroll
-        for (int e = 0; e < kE; ++e) {
-          const float xh = (cx[i].get(e) - m[i]) * r[i];
-          v[e] = (fmaf(cg[i].get(e), w[e], -c1) - xh * c2) * r[i];
+        for (int e = 0; e < kE / 2; ++e) {
+          const float2 xh =
+              kKeep ? kx[kKeep ? i : 0][kKeep ? e : 0]
+                    : fmul2(fadd2(cx[i].get2(e), ln_both(m[i])), ln_both(r[i]));
+          const float2 gw = kKeep ? kg[kKeep ? i : 0][kKeep ? e : 0] : fmul2(cg[i].get2(e), w[e]);
+          v[e] = ffma2(xh, c2, ffma2(gw, ln_both(r[i]), c1));
         }
-        ln_store<X, kC, kVec>(dx + ln_offset(p, p.ly, int(row)), lane, lanes, p.N, v);
+        ln_store<X, kC, kVec>(dx + ln_offset(p, p.ly, row), lane, lanes, p.N, v);
       }
     }
-    if (!kBlock && base + step < p.rows) fetch(base + step);
+    if (!kRing && !kBlock) fetch(t.row + t.step);
   }
   if (p.part == nullptr) return;
   // this CTA's sums: the groups of a warp by shuffles, its warps in order
   float* part = p.part + int64_t(blockIdx.x) * 2 * p.N;
+  auto value = [](const float2* v, int e) { return (e & 1) ? v[e / 2].y : v[e / 2].x; };
   if constexpr (kBlock) {
 #pragma unroll
     for (int e = 0; e < kE; ++e) {
       const int at = Frag::col(e, lane, lanes);
       if (at < p.N) {
-        part[at] = dw[e];
-        part[p.N + at] = db[e];
+        part[at] = value(dw, e);
+        part[p.N + at] = value(db, e);
       }
     }
   } else {
     const int warp = threadIdx.x >> 5;
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-      float* v = which ? db : dw;
 #pragma unroll
       for (int e = 0; e < kE; ++e) {
+        float v = value(which ? db : dw, e);
 #pragma unroll
-        for (int o = 16; o >= kLanes; o >>= 1) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o);
-        if ((threadIdx.x & 31) < kLanes) sums[warp][e * kLanes + lane] = v[e];
+        for (int o = 16; o >= kLanes; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if ((threadIdx.x & 31) < kLanes) sums[warp][e * kLanes + lane] = v;
       }
       __syncthreads();
       for (int i = threadIdx.x; i < kLanes * kE; i += kLnThreads) {

@@ -25,29 +25,35 @@ using LnKernel = void (*)(const LnParams);
 struct LnChoice {
   LnKernel kernel;
   int threads, rows;   // threads a CTA; rows a CTA takes at a time
+  int ring, ring_max;  // bytes of shared memory, and with the most threads
 };
 
-template <typename X, int kLanes, int kC, int kR, bool kVec, int kMaxThreads>
-LnKernel ln_kernel(bool bwd) {
-  return bwd ? ln_bwd_kernel<X, kLanes, kC, kR, kVec, kMaxThreads>
-             : ln_fwd_kernel<X, kLanes, kC, kR, kVec, kMaxThreads>;
+// kLanes of a warp a row (0: the CTA), kC chunks of 8 features a thread, kR
+// rows a thread at a time; registers for kFwd (kBwd) CTAs on an SM: the reductions
+// leave a CTA idle, the next one fills in.
+template <typename X, int kLanes, int kC, int kR, bool kVec, int kMaxThreads, int kFwd, int kBwd>
+LnChoice ln_form(bool bwd, int threads) {
+  const int piece = LnFrag<X, kC, kVec>::kWords * 4, tensors = bwd ? 2 : 1;
+  const int stages = kVec ? ln_stages(kMaxThreads, kR, tensors, piece) : 0;
+  return LnChoice{bwd ? ln_bwd_kernel<X, kLanes, kC, kR, kVec, kMaxThreads, kBwd>
+                      : ln_fwd_kernel<X, kLanes, kC, kR, kVec, kMaxThreads, kFwd>,
+                  threads, kLanes ? threads / kLanes * kR : kR,
+                  stages >= 2 ? stages * threads * kR * tensors * piece : 0,
+                  stages >= 2 ? stages * kMaxThreads * kR * tensors * piece : 0};
 }
 
 // The smallest form that holds a row of N features in registers.
 template <typename X, bool kVec>
 LnChoice ln_choose_x(bool bwd, int N) {
-  auto part = [&](LnKernel k, int lanes, int r) {
-    return LnChoice{k, kLnThreads, kLnThreads / lanes * r};
-  };
-  if (N <= 64) return part(ln_kernel<X, 8, 1, 4, kVec, kLnThreads>(bwd), 8, 4);
-  if (N <= 128) return part(ln_kernel<X, 16, 1, 4, kVec, kLnThreads>(bwd), 16, 4);
-  if (N <= 256) return part(ln_kernel<X, 32, 1, 4, kVec, kLnThreads>(bwd), 32, 4);
-  if (N <= 512) return part(ln_kernel<X, 32, 2, 2, kVec, kLnThreads>(bwd), 32, 2);
-  if (N <= 1024) return part(ln_kernel<X, 32, 4, 1, kVec, kLnThreads>(bwd), 32, 1);
-  const int threads = (N + 255) / 256 * 32;
-  if (threads <= 640) return LnChoice{ln_kernel<X, 0, 1, 2, kVec, 640>(bwd), threads, 2};
-  if (threads <= 1024) return LnChoice{ln_kernel<X, 0, 1, 1, kVec, 1024>(bwd), threads, 1};
-  return LnChoice{ln_kernel<X, 0, 2, 1, kVec, 1024>(bwd), (N + 511) / 512 * 32, 1};
+  if (N <= 64) return ln_form<X, 8, 1, 2, kVec, kLnThreads, 3, 2>(bwd, kLnThreads);
+  if (N <= 128) return ln_form<X, 16, 1, 2, kVec, kLnThreads, 3, 2>(bwd, kLnThreads);
+  if (N <= 256) return ln_form<X, 32, 1, 2, kVec, kLnThreads, 3, 2>(bwd, kLnThreads);
+  if (N <= 512) return ln_form<X, 32, 2, 1, kVec, kLnThreads, 2, 2>(bwd, kLnThreads);
+  if (N <= 1024) return ln_form<X, 32, 4, 1, kVec, kLnThreads, 1, 1>(bwd, kLnThreads);
+  const int threads = (N + 511) / 512 * 32;
+  if (threads <= 320) return ln_form<X, 0, 2, 1, kVec, 320, 2, 2>(bwd, threads);
+  if (threads <= 512) return ln_form<X, 0, 2, 1, kVec, 512, 1, 1>(bwd, threads);
+  return ln_form<X, 0, 2, 1, kVec, 1024, 1, 1>(bwd, threads);
 }
 LnChoice ln_choose(bool bwd, bool bf16, bool vec, int N) {
   if (bf16) return vec ? ln_choose_x<uint16_t, true>(bwd, N) : ln_choose_x<uint16_t, false>(bwd, N);
@@ -56,17 +62,28 @@ LnChoice ln_choose(bool bwd, bool bf16, bool vec, int N) {
 
 // CTAs of a launch: enough for all rows, at most what the device holds at once
 // (every CTA then walks over rows and reads the parameters once).
+// A kernel's shared-memory limit is raised on its first use on a device (and
+// again after vidattn_release).
+struct LnReady {
+  int epoch = -1, per_sm = 0;
+};
 std::mutex g_ln_mu;
-std::map<std::pair<int, std::pair<LnKernel, int>>, int> g_ln_resident;
+std::map<std::pair<int, std::pair<LnKernel, int>>, LnReady> g_ln_ready;
 int ln_grid(int dev, int sms, const LnChoice& c, int64_t rows) {
+  const int now = host::epoch();
   int per_sm = 0;
   {
     std::lock_guard<std::mutex> lk(g_ln_mu);
-    int& known = g_ln_resident[{dev, {c.kernel, c.threads}}];
-    if (known == 0 && cudaOccupancyMaxActiveBlocksPerMultiprocessor(&known, c.kernel, c.threads,
-                                                                    0) != cudaSuccess)
-      known = 0;
-    per_sm = known;
+    LnReady& r = g_ln_ready[{dev, {c.kernel, c.threads}}];
+    if (r.epoch != now) {
+      if (cudaFuncSetAttribute(c.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               c.ring_max) != cudaSuccess ||
+          cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r.per_sm, c.kernel, c.threads, c.ring) !=
+              cudaSuccess)
+        return 0;
+      r.epoch = now;
+    }
+    per_sm = r.per_sm;
   }
   if (per_sm < 1) return 0;
   return int(std::min<int64_t>((rows + c.rows - 1) / c.rows, int64_t(sms) * per_sm));
@@ -87,7 +104,11 @@ bool ln_vector(const void* p, const int64_t s[3], int item) {
   return host::aligned(p, 16) && s[0] * item % 16 == 0 && s[1] * item % 16 == 0 &&
          s[2] * item % 16 == 0;
 }
-LnLayout ln_layout(const int64_t s[3]) { return LnLayout{s[0], s[1], s[2]}; }
+LnLayout ln_layout(int B, int H, int S, const int64_t s[3]) {
+  const bool heads = H == 1 || s[1] == S * s[2];
+  const bool batch = B == 1 || (heads && s[0] == (H == 1 ? S * s[2] : H * s[1]));
+  return LnLayout{s[0], s[1], s[2], (S > 1 || (B == 1 && H == 1)) && heads && batch && s[2] <= INT_MAX};
+}
 
 bool ln_sizes_ok(int B, int H, int S, int N) {
   return B >= 1 && H >= 1 && S >= 0 && N >= 1 && N <= kLnMaxN &&
@@ -130,19 +151,20 @@ VIDATTN_API int vidattn_layernorm(const void* x, const void* weight, const void*
   p.y = y;
   p.mean = mean;
   p.rstd = rstd;
-  p.lx = ln_layout(x_strides);
-  p.ly = ln_layout(y_strides);
+  p.lx = ln_layout(B, H, S, x_strides);
+  p.ly = ln_layout(B, H, S, y_strides);
   p.rows = B * H * S;
   p.N = N;
   p.div_s = make_fastdiv(uint32_t(S));
   p.div_h = make_fastdiv(uint32_t(H));
   p.params_bf16 = param_type == VIDATTN_BF16;
+  p.inv_n = 1.f / float(N);
   p.eps = float(eps);
   const bool vec = N % 8 == 0 && ln_vector(x, x_strides, item) && ln_vector(y, y_strides, item);
   const LnChoice c = ln_choose(false, x_type == VIDATTN_BF16, vec, N);
   const int grid = ln_grid(dev, sms, c, p.rows);
   if (grid < 1) return VIDATTN_ERR_CUDA;
-  c.kernel<<<grid, c.threads, 0, reinterpret_cast<cudaStream_t>(stream_)>>>(p);
+  c.kernel<<<grid, c.threads, c.ring, reinterpret_cast<cudaStream_t>(stream_)>>>(p);
   return cudaGetLastError() == cudaSuccess ? VIDATTN_OK : VIDATTN_ERR_CUDA;
 }
 
@@ -197,21 +219,22 @@ VIDATTN_API int vidattn_layernorm_bwd(const void* dy, const void* x, const float
   p.mean = const_cast<float*>(mean);
   p.rstd = const_cast<float*>(rstd);
   p.part = params ? static_cast<float*>(workspace) : nullptr;
-  p.lx = ln_layout(x_strides);
-  p.ldy = ln_layout(dy_strides);
-  p.ly = ln_layout(dx_strides);
+  p.lx = ln_layout(B, H, S, x_strides);
+  p.ldy = ln_layout(B, H, S, dy_strides);
+  p.ly = ln_layout(B, H, S, dx_strides);
   p.rows = B * H * S;
   p.N = N;
   p.div_s = make_fastdiv(uint32_t(S));
   p.div_h = make_fastdiv(uint32_t(H));
   p.params_bf16 = param_type == VIDATTN_BF16;
+  p.inv_n = 1.f / float(N);
   const bool vec = N % 8 == 0 && ln_vector(x, x_strides, item) && ln_vector(dy, dy_strides, item) &&
                    ln_vector(dx, dx_strides, item);
   const LnChoice c = ln_choose(true, x_type == VIDATTN_BF16, vec, N);
   int grid = ln_grid(dev, sms, c, p.rows);
   if (grid < 1) return VIDATTN_ERR_CUDA;
   grid = int(std::min<int64_t>(grid, ln_bwd_parts(c, p.rows)));
-  c.kernel<<<grid, c.threads, 0, stream>>>(p);
+  c.kernel<<<grid, c.threads, c.ring, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return VIDATTN_ERR_CUDA;
   if (params) {
     const unsigned blocks = (2 * N + 31) / 32;
