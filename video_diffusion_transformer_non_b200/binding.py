@@ -102,12 +102,12 @@ def status_string(status: int) -> str:
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
+    try:
         return x.data_ptr()
+    except AttributeError:
+        pass
     if hasattr(x, "ctypes"):          # numpy array (host buffer)
         return x.ctypes.data
     raise TypeError(f"cannot take a pointer of {type(x)}")
@@ -284,23 +284,25 @@ def bwd_workspace(has_ids, B, H, S_q, S_kv, D, flags=0) -> int:
                                                 int(S_kv), int(D), int(flags))
 
 
-@contextlib.contextmanager
-def _on(tensor, stream):
-    """Makes the tensor's device current, and allocations belong to the stream
-    the work goes to (the current stream of that device by default); yields
-    that stream's handle."""
+_HERE = contextlib.nullcontext()
+
+
+def _place(tensor, stream):
+    """Where a call on ``tensor`` runs: (the stream's handle, a context in which
+    the tensor's device is current and allocations belong to that stream).
+    The default is the current stream of the tensor's device."""
     import torch
-    with torch.cuda.device(tensor.device):
-        if stream is None:
-            yield torch.cuda.current_stream().cuda_stream
-            return
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=tensor.device) if stream \
-                else torch.cuda.default_stream(tensor.device)
-        if stream.device != tensor.device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {tensor.device}")
-        with torch.cuda.stream(stream):
-            yield stream.cuda_stream
+    device = tensor.device
+    if stream is None:
+        here = torch.cuda.current_device() == device.index
+        return (torch._C._cuda_getCurrentRawStream(device.index),
+                _HERE if here else torch.cuda.device(device))
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream \
+            else torch.cuda.default_stream(device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    return stream.cuda_stream, torch.cuda.stream(stream)   # makes its device current too
 
 
 def attention_bwd(dout, q, k, v, out, lse, seg_q=None, seg_kv=None, scale=None, causal=False,
@@ -327,7 +329,8 @@ def attention_bwd(dout, q, k, v, out, lse, seg_q=None, seg_kv=None, scale=None, 
         scale = D ** -0.5
     flags = (VIDATTN_CAUSAL if causal else 0) | VIDATTN_SPLIT_KV(n_split)
     n = bwd_workspace(seg_q is not None, B, H, S_q, S_kv, D, flags)
-    with _on(q, stream) as handle:
+    handle, place = _place(q, stream)
+    with place:
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         ws = torch.empty(max(n, 0), dtype=torch.uint8, device=q.device)
         st = vidattn_bwd(q, k, v, out, dout, lse, dlse, seg_q, seg_kv, dq, dk, dv, B, H, S_q, S_kv,
@@ -387,10 +390,13 @@ def _rows(name, t, shape=None):
         raise ValueError(f"{name} must be {tuple(shape)} (is {tuple(t.shape)})")
     if t.stride(-1) != 1 and t.shape[-1] != 1:
         raise ValueError(f"the last dim of {name} must be contiguous")
-    pad = 4 - t.dim()
-    sizes = (1,) * pad + tuple(t.shape)
-    strides = (0,) * pad + tuple(t.stride())
-    return sizes, tuple(s if n > 1 else 0 for s, n in zip(strides[:3], sizes))
+    shape, strides = t.shape, t.stride()
+    if t.dim() < 4:
+        pad = 4 - t.dim()
+        shape, strides = (1,) * pad + tuple(shape), (0,) * pad + strides
+    B, H, S, N = shape
+    return (B, H, S, N), (strides[0] if B > 1 else 0, strides[1] if H > 1 else 0,
+                          strides[2] if S > 1 else 0)
 
 
 def _check_norm(x, named, weight, bias):
@@ -423,7 +429,8 @@ def layer_norm(x, weight=None, bias=None, eps=1e-6, out=None, stream=None):
     import torch
     x_type, p_type = _check_norm(x, dict(out=out), weight, bias)
     (B, H, S, N), sx = _rows("x", x)
-    with _on(x, stream) as handle:
+    handle, place = _place(x, stream)
+    with place:
         y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
         _, sy = _rows("out", y, x.shape)
         mean, rstd = (torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
@@ -451,7 +458,8 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, out=None, stream=None, params
         if t.shape != x.shape[:-1] or t.device != x.device:
             raise ValueError(f"{name} must be {tuple(x.shape[:-1])} on {x.device} (is "
                              f"{tuple(t.shape)} on {t.device})")
-    with _on(x, stream) as handle:
+    handle, place = _place(x, stream)
+    with place:
         dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
         _, sdx = _rows("out", dx, x.shape)
         dw = db = ws = None
@@ -551,7 +559,8 @@ def _rope_scaled(name, q, k, grid, bands, freqs, pos_scale, amplitude, interleav
                          f"{len(freqs)})")
     if len(pos_scale) != 3:
         raise ValueError("pos_scale must hold 3 values")
-    with _on(q, stream) as handle:
+    handle, place = _place(q, stream)
+    with place:
         if out_q is None:
             out_q = torch.empty((B, H, S, D), dtype=q.dtype, device=q.device)
         _, s_out = _rows("out_q", out_q, q.shape)

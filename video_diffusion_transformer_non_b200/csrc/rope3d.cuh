@@ -50,7 +50,9 @@ struct RopeParams {
   // kScaled only: output strides, table columns in use (the pairs of the
   // bands), and the amplitude, negative sine for the transposed rotation
   long long osb, osh, oss;
+  FastDiv div_hw, div_wg, div_hg;
   int n_cols;
+  int word_partners;   // half-split: partners of two neighbouring features are neighbours too
   float cos_mul, sin_mul;
   double freq[kRopeMaxD / 2];  // per table column: theta^(-2k/d), or the caller's
   // per feature e: its table column, its partner feature, and 1 when e is the
@@ -100,6 +102,17 @@ __global__ void __launch_bounds__(kRopeThreads) rope3d_kernel(const __grid_const
     partner_chunk[e] = p.partner[f] / 8;
     partner_elem[e] = p.partner[f] % 8;
   }
+  // kScaled, half-split: where the partners lie in the stage, in bytes.  The
+  // words of every 16-byte piece are permuted by its number (XOR), so that the
+  // 32 lanes' reads of one word meet 32 banks.
+  uint32_t at[8];
+  if constexpr (kScaled && !kInterleaved) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int slot = tid - ch + partner_chunk[e], elem = partner_elem[e];
+      at[e] = slot * 16 + ((elem / 2) ^ ((slot >> 3) & 3)) * 4 + (elem & 1) * 2;
+    }
+  }
   // kScaled: this thread's features inside the bands, as bits
   uint32_t in_bands = 0;
   if constexpr (kScaled) {
@@ -110,6 +123,32 @@ __global__ void __launch_bounds__(kRopeThreads) rope3d_kernel(const __grid_const
   int parity = 0;
   for (int tile = blockIdx.x; tile < n_tiles; tile += gridDim.x, parity ^= 1) {
     const int s0 = tile * kRopeTokens;
+    const int s = s0 + row;
+    const bool row_ok = s < p.S;
+    uint4 v[kRopeUnroll];
+    uint16_t* dst[kRopeUnroll];
+    auto load = [&](int base) {
+#pragma unroll
+      for (int u = 0; u < kRopeUnroll; ++u) {
+        const int slab = base + u * slab_step;
+        v[u] = make_uint4(0, 0, 0, 0);
+        dst[u] = nullptr;
+        if (row_ok && slab < p.n_slabs) {
+          const uint32_t t = fastdiv(uint32_t(slab), p.div_bh);
+          const uint32_t bh = uint32_t(slab) - t * p.div_bh.d;
+          const uint32_t b = fastdiv(bh, p.div_h);
+          const uint32_t h = bh - b * p.div_h.d;
+          const uint16_t* src = p.in[t] + b * p.sb + h * p.sh + s * p.ss + ch * 8;
+          if constexpr (kScaled)
+            dst[u] = p.out[t] + b * p.osb + h * p.osh + s * p.oss + ch * 8;
+          else
+            dst[u] = p.out[t] + (static_cast<long long>(bh) * p.S + s) * D + ch * 8;
+          v[u] = ld_stream_v4(src);
+        }
+      }
+    };
+    // kScaled: the first loads of a tile run beside its table
+    if (kScaled) load(slab0 + slab_lane);
     // this tile's table goes to the buffer read two tiles ago: every thread
     // has passed the previous tile's barrier, so it is done reading it
     float2 (*tb)[kHalf] = table[parity];
@@ -118,10 +157,20 @@ __global__ void __launch_bounds__(kRopeThreads) rope3d_kernel(const __grid_const
       const int n = s0 + r - p.offset;
       float cv = 1.f, sv = 0.f;
       if (n >= 0 && n < p.n_video && (!kScaled || c < p.n_cols)) {
-        const int coord = c < p.col_h ? n / p.hw : (c < p.col_w ? (n / p.Wg) % p.Hg : n % p.Wg);
         const double two_pi = 6.283185307179586476925286766559;
-        double a = double(coord) * p.freq[c];
-        a -= two_pi * rint(a / two_pi);
+        double a;
+        if constexpr (kScaled) {   // divisions by multiplication
+          const uint32_t th = fastdiv(uint32_t(n), p.div_wg);
+          const uint32_t coord = c < p.col_h   ? fastdiv(uint32_t(n), p.div_hw)
+                                 : c < p.col_w ? th - fastdiv(th, p.div_hg) * p.div_hg.d
+                                               : uint32_t(n) - th * p.div_wg.d;
+          a = double(coord) * p.freq[c];
+          a -= two_pi * rint(a * 0.15915494309189533576888376337251);
+        } else {
+          const int coord = c < p.col_h ? n / p.hw : (c < p.col_w ? (n / p.Wg) % p.Hg : n % p.Wg);
+          a = double(coord) * p.freq[c];
+          a -= two_pi * rint(a / two_pi);
+        }
         sincosf(float(a), &sv, &cv);
         if constexpr (kScaled) {
           cv *= p.cos_mul;
@@ -151,34 +200,21 @@ __global__ void __launch_bounds__(kRopeThreads) rope3d_kernel(const __grid_const
         sn[e] = first[e] ? -t.y : t.y;
       }
     }
-    const int s = s0 + row;
-    const bool row_ok = s < p.S;
     const uint32_t turned = s >= p.offset && s - p.offset < p.n_video ? in_bands : 0u;
 
     for (int base = slab0 + slab_lane; base < p.n_slabs; base += slab_step * kRopeUnroll) {
-      uint4 v[kRopeUnroll];
-      uint16_t* dst[kRopeUnroll];
-#pragma unroll
-      for (int u = 0; u < kRopeUnroll; ++u) {
-        const int slab = base + u * slab_step;
-        v[u] = make_uint4(0, 0, 0, 0);
-        dst[u] = nullptr;
-        if (row_ok && slab < p.n_slabs) {
-          const uint32_t t = fastdiv(uint32_t(slab), p.div_bh);
-          const uint32_t bh = uint32_t(slab) - t * p.div_bh.d;
-          const uint32_t b = fastdiv(bh, p.div_h);
-          const uint32_t h = bh - b * p.div_h.d;
-          const uint16_t* src = p.in[t] + b * p.sb + h * p.sh + s * p.ss + ch * 8;
-          if constexpr (kScaled)
-            dst[u] = p.out[t] + b * p.osb + h * p.osh + s * p.oss + ch * 8;
-          else
-            dst[u] = p.out[t] + (static_cast<long long>(bh) * p.S + s) * D + ch * 8;
-          v[u] = ld_stream_v4(src);
-        }
-      }
+      if (!kScaled || base != slab0 + slab_lane) load(base);
       if constexpr (!kInterleaved) {
 #pragma unroll
-        for (int u = 0; u < kRopeUnroll; ++u) stage[u][tid] = v[u];
+        for (int u = 0; u < kRopeUnroll; ++u) {
+          uint4 t = v[u];
+          if constexpr (kScaled) {
+            const int q = (tid >> 3) & 3;
+            if (q & 1) t = make_uint4(t.y, t.x, t.w, t.z);
+            if (q & 2) t = make_uint4(t.z, t.w, t.x, t.y);
+          }
+          stage[u][tid] = t;
+        }
         __syncwarp();
       }
 #pragma unroll
@@ -193,6 +229,20 @@ __global__ void __launch_bounds__(kRopeThreads) rope3d_kernel(const __grid_const
         if constexpr (kInterleaved) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) xp[e] = x[e ^ 1];
+        } else if constexpr (kScaled) {
+          const char* staged = reinterpret_cast<const char*>(stage[u]);
+          if (p.word_partners) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t t = *reinterpret_cast<const uint32_t*>(staged + at[2 * j]);
+              xp[2 * j] = bf16_lo(t);
+              xp[2 * j + 1] = bf16_hi(t);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              xp[e] = bf16_lo(*reinterpret_cast<const uint16_t*>(staged + at[e]));
+          }
         } else {
           const uint16_t* rowbase =
               reinterpret_cast<const uint16_t*>(&stage[u][tid - ch]);

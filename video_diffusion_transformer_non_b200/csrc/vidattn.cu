@@ -1022,7 +1022,11 @@ VIDATTN_API int vidattn_rope3d_scaled(const void* q_in, const void* k_in, void* 
   p.osb = out_strides[0];
   p.osh = out_strides[1];
   p.oss = out_strides[2];
+  p.div_hw = make_fastdiv(uint32_t(Hg) * uint32_t(Wg));
+  p.div_wg = make_fastdiv(uint32_t(Wg));
+  p.div_hg = make_fastdiv(uint32_t(Hg));
   p.n_cols = n_cols;
+  p.word_partners = d_t % 4 == 0 && d_h % 4 == 0 && d_w % 4 == 0;
   p.cos_mul = float(amplitude);
   p.sin_mul = (flags & VIDATTN_ROPE_TRANSPOSE) ? -p.cos_mul : p.cos_mul;
   for (int f = 0; f < D; ++f) p.partner[f] = uint8_t(f);   // behind the bands: itself
