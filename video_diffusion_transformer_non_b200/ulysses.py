@@ -24,7 +24,9 @@ The other attention forms go through the same exchange: a 3D neighbourhood
 window (each rank's token coordinates are all-gathered like the ids) and the
 3D rotary embedding, which is applied after the exchange, where each rank
 holds the whole sequence of its heads, so positions are the global ones;
-`rope_fn` replaces the rotation (tests on CPU).
+`rope_fn` replaces the rotation (tests on CPU).  The layer norm of q and k over
+each head (`qk_norm`) needs nothing of other tokens: it runs on the shard, ahead
+of the exchange; `norm_fn` replaces it (tests on CPU).
 """
 from __future__ import annotations
 
@@ -120,9 +122,18 @@ def _cuda_attention(q, k, v, seg_q, seg_kv, scale, causal, window=None):
     return binding.attention(q, k, v, seg_q, seg_kv, scale, causal=causal)
 
 
+def _cuda_norm(x, weight, bias, eps):
+    return binding.layer_norm(x, weight, bias, eps)[0]
+
+
 def _cuda_rope(q, k, rope):
     # out of place: without an exchange (one rank) q and k are views of the
     # caller's tensors, which must not change
+    if rope.get("freqs") is not None:
+        return binding.rope3d_scaled(q, k, rope["grid"], rope["bands"], rope["freqs"],
+                                     rope.get("pos_scale", (1.0, 1.0, 1.0)),
+                                     rope.get("amplitude", 1.0), rope.get("interleaved", True),
+                                     rope.get("offset", 0))
     return binding.rope3d(q, k, rope["grid"], rope["bands"], theta=rope.get("theta", 10000.0),
                           interleaved=rope.get("interleaved", True),
                           token_offset=rope.get("offset", 0))
@@ -138,7 +149,8 @@ def _all_gather_seq(x, P, group):
 
 
 def ulysses_attention(q, k, v, seg=None, scale=None, causal=False, group=None, n_chunks=1,
-                      attn_fn=None, window=None, rope=None, rope_fn=None):
+                      attn_fn=None, window=None, rope=None, rope_fn=None, qk_norm=None,
+                      norm_fn=None):
     """Attention over a sequence sharded across the ranks of `group`.
 
     q, k, v: [B, H, S/P, D] (this rank's contiguous sequence shard; H divisible
@@ -146,7 +158,10 @@ def ulysses_attention(q, k, v, seg=None, scale=None, causal=False, group=None, n
     [B, S/P] packed t << 22 | h << 11 | w of this rank's tokens, size, extent,
     clamped) for 3D neighbourhood attention, or None.  rope: dict(grid, bands,
     theta, interleaved, offset) to rotate q and k (global positions) before
-    the attention, or None.  Returns (out [B, H, S/P, D], lse fp32 [B, H, S/P])
+    the attention, or None; with freqs (and pos_scale, amplitude) in the place
+    of theta, as binding.rope3d_scaled takes them.  qk_norm: dict(q=(weight,
+    bias), k=(weight, bias), eps) to layer-norm q and k over each head ahead of
+    both, weight and bias [D] or None, or None.  Returns (out [B, H, S/P, D], lse fp32 [B, H, S/P])
     for this rank's shard, equal to the corresponding rows of single-device
     attention over the whole sequence.  Head chunk c's attention starts once
     its own inputs have arrived, while later chunks' exchanges are still in
@@ -159,6 +174,11 @@ def ulysses_attention(q, k, v, seg=None, scale=None, causal=False, group=None, n
         scale = D ** -0.5
     if window is not None and (seg is not None or causal):
         raise ValueError("a window goes without ids and without the causal limit")
+    if qk_norm is not None:
+        norm = norm_fn or _cuda_norm
+        eps = qk_norm.get("eps", 1e-6)
+        q = norm(q, *(qk_norm.get("q") or (None, None)), eps)
+        k = norm(k, *(qk_norm.get("k") or (None, None)), eps)
     attn = attn_fn or _cuda_attention
     turn = rope_fn or _cuda_rope
     seg_full = None if seg is None else _all_gather_seq(seg, P, group)
