@@ -30,6 +30,21 @@
 
 namespace vidattn {
 
+// 32 lanes x 16 columns, as tmem_ld32.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
+}
+
 constexpr int kBwdSoftmaxWarps = 16;
 constexpr int kBwdMmaWarp = 16, kBwdLoadWarp = 17;
 constexpr int kBwdThreads = 640;   // 2 warps more: registers are dealt to 4 warps at a time
@@ -221,6 +236,21 @@ __device__ __forceinline__ void bulk_load_elect(uint32_t dst, const void* src, u
       : "memory");
 }
 
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                             uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // The other-side tiles a unit walks: positions [t0, t1) of its visit sequence,
 // first + each set bit in turn (with ids), or first, first + 1, ...
 struct BwdWalk {
@@ -297,12 +327,12 @@ __device__ __forceinline__ void bwd_probs32(const uint32_t (&r)[32], float c, fl
   }
 }
 
-// dS = P (dP - delta) of the same 32 columns (r: dP), packed to bf16 pairs.
+// dS = P (dP - delta) of 16 columns (r: dP), packed to bf16 pairs.
 template <bool kPerColumn>
-__device__ __forceinline__ void bwd_dscores32(const uint32_t (&r)[32], float nd, const float* nds,
-                                              const float (&pr)[32], uint32_t (&pk)[16]) {
+__device__ __forceinline__ void bwd_dscores16(const uint32_t (&r)[16], float nd, const float* nds,
+                                              const float* pr, uint32_t* pk) {
 #pragma unroll
-  for (int x = 0; x < 32; x += 4) {
+  for (int x = 0; x < 16; x += 4) {
     float4 o = make_float4(nd, nd, nd, nd);
     if (kPerColumn) o = *reinterpret_cast<const float4*>(nds + x);
 #pragma unroll
@@ -316,11 +346,20 @@ __device__ __forceinline__ void bwd_dscores32(const uint32_t (&r)[32], float nd,
   }
 }
 
-// kCols columns of an accumulator's row from tensor memory, times mul, to bf16 (out) or
-// to fp32 (part).  have: the accumulator was written (a tile was visited).
-template <int kCols>
-__device__ __forceinline__ void bwd_store_row(uint32_t taddr, bool have, bool row_valid, float mul,
-                                              uint16_t* out, float* part) {
+// 32 rows (a warp's lanes) x kCols columns of an accumulator from tensor
+// memory, times mul, to bf16 (out) or as they are to fp32 (part), both at row
+// pitch D.  have: the accumulator was written (a tile was visited); n_rows: of
+// the 32 that exist.  A lane holds a row, so that its stores would touch 32
+// rows with 16 bytes each; by way of `stage` (32 rows of kCols * 4 + 16 bytes,
+// this warp's own) neighbouring lanes write neighbouring bytes instead (a KV
+// unit's two gradients at D = 128: 3.4 us row by row).
+template <int D, int kCols>
+__device__ __forceinline__ void bwd_store_rows(uint32_t taddr, bool have, int n_rows, float mul,
+                                               uint16_t* out, float* part, uint32_t stage) {
+  const int lane = threadIdx.x & 31;
+  const bool wide = part != nullptr;
+  const uint32_t pitch = kCols * (wide ? 4 : 2) + 16;   // 16 bytes off: rows meet other banks
+  const uint32_t mine = stage + lane * pitch;
 #pragma unroll 1
   for (int kk = 0; kk < kCols / 32; ++kk) {
     uint32_t o[32];
@@ -332,23 +371,28 @@ __device__ __forceinline__ void bwd_store_row(uint32_t taddr, bool have, bool ro
 #pragma unroll
       for (int x = 0; x < 32; ++x) o[x] = 0u;
     }
-    if (!row_valid) continue;
-    if (part) {
-      float4* dst = reinterpret_cast<float4*>(part + 32 * kk);
+    if (wide) {
 #pragma unroll
       for (int x = 0; x < 8; ++x)
-        dst[x] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
-                             __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
+        st_shared_v4(mine + kk * 128 + 16 * x, o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
     } else {
-      uint32_t w[16];
 #pragma unroll
       for (int x = 0; x < 16; ++x)
-        w[x] = pack_bf16x2(__uint_as_float(o[2 * x]) * mul, __uint_as_float(o[2 * x + 1]) * mul);
-      uint4* dst = reinterpret_cast<uint4*>(out + 32 * kk);
+        o[x] = pack_bf16x2(__uint_as_float(o[2 * x]) * mul, __uint_as_float(o[2 * x + 1]) * mul);
 #pragma unroll
       for (int x = 0; x < 4; ++x)
-        dst[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+        st_shared_v4(mine + kk * 64 + 16 * x, o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
     }
+  }
+  __syncwarp();
+  const int per_row = kCols * (wide ? 4 : 2) / 16;   // lanes that write one row
+  char* dst = wide ? reinterpret_cast<char*>(part) : reinterpret_cast<char*>(out);
+  const int64_t row_bytes = D * (wide ? 4 : 2);
+#pragma unroll 4
+  for (int i = lane; i < 32 * per_row; i += 32) {
+    const int row = i / per_row, col = i % per_row;
+    const uint4 v = ld_shared_v4(stage + row * pitch + col * 16);
+    if (row < n_rows) *reinterpret_cast<uint4*>(dst + row * row_bytes + col * 16) = v;
   }
 }
 
@@ -357,7 +401,7 @@ template <int D, bool kKV>
 __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                          const CUtensorMap& tm_v, const CUtensorMap& tm_do,
                                          const BwdParams& p, uint32_t sbase, uint8_t* smem,
-                                         uint32_t tmem, int bh, int own, int split, int n_split) {
+                                         int bh, int own, int split, int n_split) {
   using C = BwdCfg<D>;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -458,40 +502,49 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
     return kKV ? tile < edge : tile >= edge;
   };
 
+  // The load warp's work.  KV unit: K and V stay; ring A holds Q, ring B dO and
+  // the row statistics.  Q unit: Q and dO stay; ring A holds K, ring B V.
+  int n_a = 0, n_b = 0;   // loads issued
+  auto load = [&](int n, int tile, int which) {
+    const CUtensorMap* map = which ? (kKV ? &tm_do : &tm_v) : (kKV ? &tm_q : &tm_k);
+    const bool with_stats = kKV && which == 1;
+    const uint32_t full = which ? b_full(n) : a_full(n), dst = which ? sB(n) : sA(n);
+    mbar_arrive_expect_tx_elect(full, C::kTileBytes + (with_stats ? C::kStatBytes : 0));
+    for (int s = 0; s < C::kSub; ++s)
+      tma_load_3d_elect(dst + s * C::kSubBytes, map, full, s * 64, tile * 128, bh);
+    if (with_stats)
+      bulk_load_elect(sbase + C::kOffStats + (n % kB) * C::kStatBytes,
+                      p.stats + (static_cast<int64_t>(bh) * p.n_q_tiles + tile) * 256,
+                      C::kStatBytes, full);
+    if (which) n_b = n + 1;
+    else n_a = n + 1;
+  };
+  if (warp == kBwdLoadWarp && n_tiles > 0) {   // the first tiles, ahead of the CTA's set-up
+    const int tile = walk.first + walk.next(walk.start);
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const CUtensorMap* map = which ? (kKV ? &tm_v : &tm_do) : (kKV ? &tm_k : &tm_q);
+      mbar_arrive_expect_tx_elect(fixed_full(which), C::kTileBytes);
+      for (int s = 0; s < C::kSub; ++s)
+        tma_load_3d_elect(sFix[which] + s * C::kSubBytes, map, fixed_full(which), s * 64,
+                          own * 128, bh);
+      load(0, tile, which);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc);
+
   if (warp == kBwdLoadWarp) {
     // -------------------------------------------------------------- loads
-    // KV unit: K and V stay; ring A holds Q, ring B dO and the row statistics.
-    // Q unit: Q and dO stay; ring A holds K, ring B V.
-    const CUtensorMap* fixed_map[2] = {kKV ? &tm_k : &tm_q, kKV ? &tm_v : &tm_do};
-    const CUtensorMap* ring_map[2] = {kKV ? &tm_q : &tm_k, kKV ? &tm_do : &tm_v};
     bool ok = true;
-    int n_a = 0, n_b = 0;   // loads issued
-    for (int n = 0, pos = walk.start; n < n_tiles && ok; ++n, ++pos) {
+    for (int n = 1, pos = n_tiles > 0 ? walk.next(walk.start) + 1 : 0; n < n_tiles && ok; ++n, ++pos) {
       pos = walk.next(pos);
-      const int tile = walk.first + pos;
-#pragma unroll
-      for (int which = 0; which < 2; ++which) {
-        if (n == 0) {
-          mbar_arrive_expect_tx_elect(fixed_full(which), C::kTileBytes);
-          for (int s = 0; s < C::kSub; ++s)
-            tma_load_3d_elect(sFix[which] + s * C::kSubBytes, fixed_map[which], fixed_full(which),
-                              s * 64, own * 128, bh);
-        }
-        const uint32_t full = which ? b_full(n) : a_full(n);
+      for (int which = 0; which < 2 && ok; ++which) {
         ok = warp_wait_phase(which ? b_empty(n) : a_empty(n), (which ? b_par(n) : a_par(n)) ^ 1u,
                              abort_flag, p.err);
-        if (!ok) break;
-        const bool with_stats = kKV && which == 1;
-        mbar_arrive_expect_tx_elect(full, C::kTileBytes + (with_stats ? C::kStatBytes : 0));
-        const uint32_t dst = which ? sB(n) : sA(n);
-        for (int s = 0; s < C::kSub; ++s)
-          tma_load_3d_elect(dst + s * C::kSubBytes, ring_map[which], full, s * 64, tile * 128, bh);
-        if (with_stats)
-          bulk_load_elect(sbase + C::kOffStats + (n % kB) * C::kStatBytes,
-                          p.stats + (static_cast<int64_t>(bh) * p.n_q_tiles + tile) * 256,
-                          C::kStatBytes, full);
-        if (which) n_b = n + 1;
-        else n_a = n + 1;
+        if (ok) load(n, walk.first + pos, which);
       }
     }
     if (!ok) {
@@ -626,32 +679,41 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
                : bwd_wait(s_full, uint32_t(n) & 1u, abort_flag, p.err);
       if (!ok) break;
       tc_fence_after();
-      uint32_t rr[32], pk[16];
       float pr[32];
-      tmem_ld32(tS, rr);
-      tmem_ld_wait();
-      reg_fence(rr);
-      arrive(s_free);
-      bwd_probs32<kKV>(rr, p.c, nlse, stats, pr);
+      {
+        uint32_t rr[32];
+        tmem_ld32(tS, rr);
+        tmem_ld_wait();
+        reg_fence(rr);
+        arrive(s_free);
+        bwd_probs32<kKV>(rr, p.c, nlse, stats, pr);
+      }
       if (masked) {
 #pragma unroll
         for (int x = 0; x < 32; ++x) pr[x] = (vis >> x) & 1 ? pr[x] : 0.f;
       }
+      ok = wait(dp_full(n), dp_par(n));
+      if (!ok) break;
+      // P goes over the first 16 columns of dP, dS over the other 16, each once
+      // they are in registers
+      uint32_t rd[16], pk[16];
+      tmem_ld16(tX, rd);
       if (kKV) {
 #pragma unroll
         for (int x = 0; x < 16; ++x) pk[x] = pack_bf16x2(pr[2 * x], pr[2 * x + 1]);
       }
-      ok = wait(dp_full(n), dp_par(n));
-      if (!ok) break;
-      tmem_ld32(tX, rr);
       tmem_ld_wait();
-      reg_fence(rr);
-      if (kKV) tmem_st16(tX, pk);   // over the dP just read
+      reg_fence16(rd);
+      if (kKV) tmem_st16(tX, pk);
+      bwd_dscores16<kKV>(rd, ndelta, stats + 128, pr, pk);
+      tmem_ld16(tX + 16, rd);
       if (kKV && kX == 1) {
         tmem_st_wait();
         arrive(p_full);
       }
-      bwd_dscores32<kKV>(rr, ndelta, stats + 128, pr, pk);
+      tmem_ld_wait();
+      reg_fence16(rd);
+      bwd_dscores16<kKV>(rd, ndelta, stats + 144, pr + 16, pk + 8);
       tmem_st16(tX + 16, pk);
       tmem_st_wait();
       arrive(ds_full(n));
@@ -660,22 +722,30 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
     ok = ok && warp_wait_phase(done, 0, abort_flag, p.err);
     if (ok) {
       tc_fence_after();
+      // every load and product is over: the rings are free to stage the stores
       const bool have = n_tiles > 0;
+      const int row0 = own * 128 + 32 * (warp & 3);   // this warp's first row
+      constexpr int kStage = 32 * ((kKV ? D / 2 : 32) * 4 + 16);
+      static_assert(kBwdSoftmaxWarps * kStage <= (C::kStagesA + C::kStagesB) * C::kTileBytes,
+                    "stages in the rings");
+      const uint32_t stage = sbase + C::kOffRingA + warp * kStage;
       if (kKV) {   // a quarter of the warps each: the halves of dV's and of dK's columns
-        const bool dk = quarter >= 2;
+        const bool is_dk = quarter >= 2;
         const int col = (quarter & 1) * (D / 2);
-        const int64_t at = (static_cast<int64_t>(bh) * p.S_kv + row) * D + col;
+        const int64_t at = (static_cast<int64_t>(bh) * p.S_kv + row0) * D + col;
         float* part = nullptr;
         if (n_split > 1)
-          part = p.part_kv + (int64_t(split) * 2 + (dk ? 0 : 1)) * p.BH * p.S_kv * D + at;
-        bwd_store_row<D / 2>(tLane + (dk ? C::kTmemAcc1 : C::kTmemAcc0) + col, have, row < p.S_kv,
-                             dk ? p.scale : 1.f, (dk ? p.dk : p.dv) + at, part);
+          part = p.part_kv + (int64_t(split) * 2 + (is_dk ? 0 : 1)) * p.BH * p.S_kv * D + at;
+        bwd_store_rows<D, D / 2>(tLane + (is_dk ? C::kTmemAcc1 : C::kTmemAcc0) + col, have,
+                                 min(p.S_kv - row0, 32), is_dk ? p.scale : 1.f,
+                                 (is_dk ? p.dk : p.dv) + at, part, stage);
       } else if (quarter < D / 32) {   // 32 of dQ's columns each
         const int col = 32 * quarter;
-        const int64_t at = (static_cast<int64_t>(bh) * p.S_q + row) * D + col;
+        const int64_t at = (static_cast<int64_t>(bh) * p.S_q + row0) * D + col;
         float* part = nullptr;
         if (n_split > 1) part = p.part_q + int64_t(split) * p.BH * p.S_q * D + at;
-        bwd_store_row<32>(tLane + C::kTmemAcc0 + col, have, row < p.S_q, p.scale, p.dq + at, part);
+        bwd_store_rows<D, 32>(tLane + C::kTmemAcc0 + col, have, min(p.S_q - row0, 32), p.scale,
+                              p.dq + at, part, stage);
       }
     }
   }
@@ -704,36 +774,39 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
-  if (threadIdx.x == 0) {
-    auto bar = [&](int i) { return sbase + C::kOffBar + 8 * i; };
-    constexpr int kBars = 2 + 2 * (C::kStagesA + C::kStagesB);
-    for (int i = 0; i < C::kNumBars; ++i) {
-      mbar_init(bar(i), i >= kBars + 4 ? kBwdSoftmaxWarps : 1);
+  // the load warp sets up the barriers, so that its first loads need not wait
+  // for the other warps
+  if (warp == kBwdLoadWarp) {
+    if ((threadIdx.x & 31) == 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+      tma_prefetch_desc(&tm_do);
+      for (int i = 0; i < C::kNumBars; ++i)
+        mbar_init(sbase + C::kOffBar + 8 * i,
+                  i >= 2 + 2 * (C::kStagesA + C::kStagesB) + 4 ? kBwdSoftmaxWarps : 1);
+      *reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4) = 0;
+      fence_mbar_init();
     }
-    *reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4) = 0;
-    fence_mbar_init();
+    __syncwarp();
   }
   if (warp == kBwdMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
     tmem_relinquish();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
   int u = blockIdx.x;
   if (u < p.n_kv_units) {
     const int split = u % p.n_kv_split;
     u /= p.n_kv_split;
-    bwd_unit<D, true>(tm_q, tm_k, tm_v, tm_do, p, sbase, smem, tmem, u / p.n_kv_tiles,
+    bwd_unit<D, true>(tm_q, tm_k, tm_v, tm_do, p, sbase, smem, u / p.n_kv_tiles,
                             u % p.n_kv_tiles, split, p.n_kv_split);
   } else {
     u -= p.n_kv_units;
     const int split = u % p.n_q_split;
     u /= p.n_q_split;
     const int t = u % p.n_q_tiles;
-    bwd_unit<D, false>(tm_q, tm_k, tm_v, tm_do, p, sbase, smem, tmem, u / p.n_q_tiles,
+    bwd_unit<D, false>(tm_q, tm_k, tm_v, tm_do, p, sbase, smem, u / p.n_q_tiles,
                              p.causal ? p.n_q_tiles - 1 - t : t, split, p.n_q_split);
   }
 
@@ -741,7 +814,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __syncthreads();
   if (warp == kBwdMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::kTmemCols);
+    tmem_dealloc(*reinterpret_cast<volatile uint32_t*>(tmem_slot), C::kTmemCols);
   }
 }
 
