@@ -223,6 +223,9 @@ __device__ __forceinline__ void ln_params(const void* src, int bf16, int lane, i
   } else {
     ln_params_of<float, kC, kVec>(static_cast<const float*>(src), lane, lanes, N, v);
   }
+  // kept in registers, not read again for every row
+#pragma unroll
+  for (int e = 0; e < 4 * kC; ++e) asm volatile("" : "+f"(v[e].x), "+f"(v[e].y));
 }
 
 // Sums over the lanes of a row: a part of a warp, or the CTA (kBlock), whose
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_bwd_kernel(const LnPara
   constexpr bool kBlock = Walk::kBlock, kRing = Walk::kRing;
   constexpr int kE = 8 * kC, kS = Walk::kS;
   // xh and g are kept from the sums to the result where registers allow
-  constexpr bool kKeep = kE * kR <= 16 && kMaxThreads <= 320;
+  constexpr bool kKeep = kC == 1 && kR <= 2 && kMaxThreads <= 320;
   __shared__ __align__(16) float buf[kBlock ? 2 : 1][2 * kR][32];
   if (kBlock) {
     for (int i = threadIdx.x; i < 4 * kR * 32; i += blockDim.x) (&buf[0][0][0])[i] = 0.f;
