@@ -134,13 +134,14 @@ def _check_tensors(named, dtype, ndim=None, contiguous=True):
             continue
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} must be a torch tensor, not {type(t).__name__}")
-        if t.device.type != _DEVICE_TYPE:
-            raise ValueError(f"{name} must be on a CUDA device (is on {t.device})")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
-        if t.dtype != dtype:
+        here = t.device
+        if here != device:
+            if here.type != _DEVICE_TYPE:
+                raise ValueError(f"{name} must be on a CUDA device (is on {here})")
+            if device is not None:
+                raise ValueError(f"{name} is on {here}, the other tensors on {device}")
+            device = here
+        if t.dtype is not dtype:
             raise ValueError(f"{name} must be {dtype} (is {t.dtype})")
         if ndim is not None and t.dim() != ndim:
             raise ValueError(f"{name} must have {ndim} dims (has shape {tuple(t.shape)})")
@@ -332,7 +333,7 @@ def attention_bwd(dout, q, k, v, out, lse, seg_q=None, seg_kv=None, scale=None, 
     handle, place = _place(q, stream)
     with place:
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        ws = torch.empty(max(n, 0), dtype=torch.uint8, device=q.device)
+        ws = q.new_empty(max(n, 0), dtype=torch.uint8)
         st = vidattn_bwd(q, k, v, out, dout, lse, dlse, seg_q, seg_kv, dq, dk, dv, B, H, S_q, S_kv,
                          D, scale, flags, ws if n > 0 else None, n, handle)
     if st != VIDATTN_OK:
@@ -399,6 +400,12 @@ def _rows(name, t, shape=None):
                           strides[2] if S > 1 else 0)
 
 
+def _like(t):
+    """An uninitialised contiguous tensor of t's shape, type and device."""
+    import torch
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _check_norm(x, named, weight, bias):
     """Common checks of layer_norm and layer_norm_bwd; returns the types."""
     import torch
@@ -431,10 +438,9 @@ def layer_norm(x, weight=None, bias=None, eps=1e-6, out=None, stream=None):
     (B, H, S, N), sx = _rows("x", x)
     handle, place = _place(x, stream)
     with place:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-        _, sy = _rows("out", y, x.shape)
-        mean, rstd = (torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-                      for _ in range(2))
+        y = _like(x) if out is None else out
+        sy = _rows("out", y, x.shape)[1]
+        mean, rstd = x.new_empty((2, *x.shape[:-1]), dtype=torch.float32).unbind(0)
         if x.numel() == 0 and N > 0:
             return y, mean, rstd
         st = vidattn_layernorm(x, weight, bias, y, mean, rstd, B, H, S, N, sx, sy, x_type, p_type,
@@ -460,8 +466,8 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, out=None, stream=None, params
                              f"{tuple(t.shape)} on {t.device})")
     handle, place = _place(x, stream)
     with place:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-        _, sdx = _rows("out", dx, x.shape)
+        dx = _like(x) if out is None else out
+        sdx = _rows("out", dx, x.shape)[1]
         dw = db = ws = None
         n = 0
         if weight is not None and params:
@@ -469,7 +475,7 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, out=None, stream=None, params
             if x.numel() == 0:
                 return dx, dw.zero_(), db.zero_()
             n = layernorm_bwd_workspace(B, H, S, N, x_type)
-            ws = torch.empty(max(n, 0), dtype=torch.uint8, device=x.device)
+            ws = x.new_empty(max(n, 0), dtype=torch.uint8)
         if x.numel() == 0 and N > 0:
             return dx, None, None
         st = vidattn_layernorm_bwd(dy, x, mean, rstd, weight, dx, dw, db, B, H, S, N, sdy, sx, sdx,
@@ -562,12 +568,14 @@ def _rope_scaled(name, q, k, grid, bands, freqs, pos_scale, amplitude, interleav
     handle, place = _place(q, stream)
     with place:
         if out_q is None:
-            out_q = torch.empty((B, H, S, D), dtype=q.dtype, device=q.device)
-        _, s_out = _rows("out_q", out_q, q.shape)
+            out_q = _like(q)
+        s_out = _rows("out_q", out_q, q.shape)[1]
         if k is not None:
             if out_k is None:
-                out_k = torch.empty_strided(out_q.shape, out_q.stride(), dtype=k.dtype,
-                                            device=k.device)
+                out_k = torch.empty_like(out_q)   # of a dense out_q: the same strides
+                if out_k.stride() != out_q.stride():
+                    out_k = torch.empty_strided(out_q.shape, out_q.stride(), dtype=k.dtype,
+                                                device=k.device)
             if _rows("out_k", out_k, q.shape)[1] != s_out:
                 raise ValueError("out_q and out_k must have the same strides")
         if q.numel() == 0 and D > 0:
