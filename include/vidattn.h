@@ -30,7 +30,9 @@
  * throw.  Status codes are the vidattn_status values below.
  *
  * CUDA graphs: once set up, vidattn_fwd, vidattn_fwd_ex, vidattn_fwd_window,
- * vidattn_fwd_noalloc and vidattn_rope3d enqueue kernel launches on `stream`
+ * vidattn_fwd_noalloc, vidattn_rope3d and vidattn_rope3d_scaled, vidattn_bwd and
+ * the layer norm's calls enqueue kernel launches (memsets where there is nothing
+ * to compute) on `stream`
  * and nothing else, so they can be captured into a graph.  Set-up happens on
  * the first call on a device (kernel attributes, symbol addresses, occupancy
  * queries: host calls only) and, for the calls that use scratch (ids or a

@@ -160,6 +160,15 @@ def test_joint_sequence():
     run(x)
 
 
+def test_more_tiles_than_a_unit_lists():
+    """With ids and more query tiles than a unit keeps as bits (3072), it walks
+    every tile of its range and masks them all."""
+    S_q = 3100 * 128 + 5
+    x = make(1, 1, S_q, 200, 64, 7500, "runs")
+    run(x)
+    run(x, causal=True)
+
+
 def test_after_the_forward_kernel():
     """binding.attention's own out and lse, equal ids and strides; the same
     bits from a second call, from another stream, and with a head on its own."""

@@ -29,10 +29,19 @@ def _grad(g, like):
     return torch.zeros_like(like) if g is None else g.contiguous()
 
 
+def _attention_on(q, k, v, seg_q, seg_kv, scale, causal):
+    """binding.attention on q's device and its current stream, whichever device
+    is current."""
+    if not q.is_cuda or torch.cuda.current_device() == q.device.index:
+        return binding.attention(q, k, v, seg_q, seg_kv, scale, causal=causal)
+    with torch.cuda.device(q.device):
+        return binding.attention(q, k, v, seg_q, seg_kv, scale, causal=causal)
+
+
 class _Attention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, seg_q, seg_kv, scale, causal):
-        out, lse = binding.attention(q, k, v, seg_q, seg_kv, scale, causal=causal)
+        out, lse = _attention_on(q, k, v, seg_q, seg_kv, scale, causal)
         ctx.save_for_backward(q, k, v, out, lse, seg_q, seg_kv)
         ctx.set_materialize_grads(False)
         ctx.scale, ctx.causal = scale, causal
@@ -131,7 +140,7 @@ class _QkvAttention(torch.autograd.Function):
             qn, kn = binding.rope3d_scaled(qn, kn, **turn,
                                            **(dict(out_q=qn, out_k=kn) if norm else {}))
         qn, kn, vn = qn.contiguous(), kn.contiguous(), v.contiguous()
-        out, lse = binding.attention(qn, kn, vn, seg_q, seg_kv, scale, causal=causal)
+        out, lse = _attention_on(qn, kn, vn, seg_q, seg_kv, scale, causal)
         ctx.save_for_backward(*((q, k) if norm else (None, None)), wq, wk, *stats, qn, kn, vn, out,
                               lse, seg_q, seg_kv)
         ctx.turn, ctx.scale, ctx.causal, ctx.norm = turn, scale, causal, norm

@@ -188,6 +188,20 @@ struct Scratch {
 };
 std::map<std::pair<int, cudaStream_t>, Scratch> g_scratch;
 
+// Makes the device's context current in this thread: a new thread has none
+// until a runtime call that needs one, and the tensor maps are encoded by a
+// driver call, which fails without.  A host query, once per thread and device
+// (and again after vidattn_release).  Called with g_mu held.
+bool bind_thread(int dev) {
+  static thread_local int bound_dev = -1, bound_epoch = -1;
+  if (bound_dev == dev && bound_epoch == g_epoch) return true;
+  cudaFuncAttributes attr;
+  if (cudaFuncGetAttributes(&attr, fwd_variant<64>(0)) != cudaSuccess) return false;
+  bound_dev = dev;
+  bound_epoch = g_epoch;
+  return true;
+}
+
 int ensure_device(int* dev_out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return VIDATTN_ERR_CUDA;
@@ -205,6 +219,7 @@ int ensure_device(int* dev_out) {
       return VIDATTN_ERR_CUDA;
   }
   if (!info.ok) return VIDATTN_ERR_NO_DEVICE;
+  if (!bind_thread(dev)) return VIDATTN_ERR_CUDA;
   if (info.err == nullptr) {
     void* e = nullptr;
     if (cudaGetSymbolAddress(&e, g_device_error) != cudaSuccess || e == nullptr)
