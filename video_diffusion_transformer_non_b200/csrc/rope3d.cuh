@@ -8,13 +8,13 @@
 // outside the video range are copied unchanged.  include/vidattn.h
 // (vidattn_rope3d) states the argument contract.
 //
-// Work split: a tile is kRopeTokens consecutive tokens of every (tensor, b, h)
+// Work split: a tile is 8 (or 16) consecutive tokens of every (tensor, b, h)
 // slab.  The CTA computes the tile's (cos, sin) table once in shared memory
 // (the angles in fp64, reduced to [-pi, pi], then sincosf; two tables
 // alternate, so one barrier per tile suffices), each thread keeps the entries
 // of its own 8 features in registers and then streams 16-byte chunks of all
-// slabs through them: 8 loads in flight per thread (4 with the half-split
-// pairing, whose staging needs more registers), streaming-cache loads and
+// slabs through them: 4 or 8 loads in flight per thread (rope_unroll below),
+// streaming-cache loads and
 // stores (every byte is touched once).  The
 // interleaved pairing finds both features of a pair in one chunk; the
 // half-split pairing stages the chunk in shared memory and reads the partner
@@ -35,7 +35,16 @@
 namespace vidattn {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeTokens = 8;
+// Tokens of a tile, and 16-byte loads in flight a thread.  kScaled, measured on
+// 480p q and k (interleaved) and on 2 x 8 heads of 18452 x 64 (half-split):
+// 8 tokens and 4 loads 232 us (8 loads 238, 16 tokens 270); 16 tokens and 8
+// loads 39 us (8 tokens and 4 loads 45, 8 and 8: 57).
+__host__ __device__ constexpr int rope_tokens(bool interleaved, bool scaled) {
+  return scaled && !interleaved ? 16 : 8;
+}
+__host__ __device__ constexpr int rope_unroll(bool interleaved, bool scaled) {
+  return interleaved != scaled ? 8 : 4;
+}
 constexpr int kRopeMaxD = 128;
 
 struct RopeParams {
@@ -71,12 +80,13 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 
 template <int D, bool kInterleaved, bool kScaled>
 __global__ void __launch_bounds__(kRopeThreads) rope3d_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int kRopeTokens = rope_tokens(kInterleaved, kScaled);
   constexpr int kHalf = D / 2;
   constexpr int kChunks = D / 8;                           // 16-byte chunks per row
   constexpr int kPerSlab = kRopeTokens * kChunks;          // threads per slab
   constexpr int kSlabsPerPass = kRopeThreads / kPerSlab;
   static_assert(kRopeThreads % kPerSlab == 0 && 32 % kChunks == 0, "tile shape");
-  constexpr int kRopeUnroll = kInterleaved ? 8 : 4;   // 16-byte loads in flight per thread
+  constexpr int kRopeUnroll = rope_unroll(kInterleaved, kScaled);
 
   __shared__ __align__(16) float2 table[2][kRopeTokens][kHalf];
   __shared__ uint4 stage[kInterleaved ? 1 : kRopeUnroll][kRopeThreads];

@@ -982,7 +982,8 @@ VIDATTN_API int vidattn_rope3d(const void* q_in, const void* k_in, void* q_out, 
   const int variant = (D == 128 ? 2 : 0) + (half_split ? 1 : 0);
   const int grid_max = rope_grid(dev, variant);
   if (grid_max <= 0) return VIDATTN_ERR_CUDA;
-  const int n_tiles = (S + kRopeTokens - 1) / kRopeTokens;
+  const int tokens = rope_tokens(!half_split, false);
+  const int n_tiles = (S + tokens - 1) / tokens;
   const int grid = n_tiles < grid_max ? n_tiles : grid_max;
   rope_variant(variant)<<<grid, kRopeThreads, 0, reinterpret_cast<cudaStream_t>(stream_)>>>(p);
   return cudaGetLastError() == cudaSuccess ? VIDATTN_OK : VIDATTN_ERR_CUDA;
@@ -1050,8 +1051,9 @@ VIDATTN_API int vidattn_rope3d_scaled(const void* q_in, const void* k_in, void* 
   const int variant = 4 + (D == 128 ? 2 : 0) + (half_split ? 1 : 0);
   const int grid_max = rope_grid(dev, variant);
   if (grid_max <= 0) return VIDATTN_ERR_CUDA;
-  const int n_tiles = (S + kRopeTokens - 1) / kRopeTokens;
-  const int per_pass = kRopeThreads / (kRopeTokens * (D / 8));   // slabs a CTA takes at once
+  const int tokens = rope_tokens(!half_split, true);
+  const int n_tiles = (S + tokens - 1) / tokens;
+  const int per_pass = kRopeThreads / (tokens * (D / 8));   // slabs a CTA takes at once
   const int passes = (p.n_slabs + per_pass - 1) / per_pass;
   dim3 grid(n_tiles < grid_max ? n_tiles : grid_max, 1);
   grid.y = std::min(std::max(grid_max / int(grid.x), 1), std::min(passes, 65535));
