@@ -319,10 +319,10 @@ def attention_bwd(dout, q, k, v, out, lse, seg_q=None, seg_kv=None, scale=None, 
     S_kv = k.shape[2]
     _check_tensors(dict(q=q, dout=dout, out=out), torch.bfloat16, ndim=4)
     _check_tensors(dict(lse=lse, dlse=dlse), torch.float32, ndim=3)
-    for name, t, shape in (("dout", dout, (B, H, S_q, D)), ("out", out, (B, H, S_q, D)),
-                           ("lse", lse, (B, H, S_q)), ("dlse", dlse, (B, H, S_q))):
-        if t is not None and tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be {shape} (is {tuple(t.shape)})")
+    for name, t, shape in (("dout", dout, q.shape), ("out", out, q.shape),
+                           ("lse", lse, q.shape[:3]), ("dlse", dlse, q.shape[:3])):
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{name} must be {tuple(shape)} (is {tuple(t.shape)})")
     if lse.device != q.device:
         raise ValueError(f"lse is on {lse.device}, q on {q.device}")
     _check_per_token("seg_q", seg_q, "seg_kv", seg_kv, B, S_q, S_kv, q.device)
@@ -344,8 +344,11 @@ def attention_bwd(dout, q, k, v, out, lse, seg_q=None, seg_kv=None, scale=None, 
 VIDATTN_BF16, VIDATTN_F32 = 0, 1
 
 
+_Strides = ctypes.c_int64 * 3
+
+
 def _strides(values):
-    return (ctypes.c_int64 * 3)(*values)
+    return _Strides(*values)
 
 
 def vidattn_layernorm(x, weight, bias, y, mean, rstd, B, H, S, N, x_strides, y_strides, x_type,
@@ -376,10 +379,11 @@ def layernorm_bwd_workspace(B, H, S, N, x_type) -> int:
 
 def _type_code(t):
     import torch
-    codes = {torch.bfloat16: VIDATTN_BF16, torch.float32: VIDATTN_F32}
-    if t not in codes:
-        raise ValueError(f"dtype must be bfloat16 or float32 (is {t})")
-    return codes[t]
+    if t is torch.bfloat16:
+        return VIDATTN_BF16
+    if t is torch.float32:
+        return VIDATTN_F32
+    raise ValueError(f"dtype must be bfloat16 or float32 (is {t})")
 
 
 def _rows(name, t, shape=None):
