@@ -207,7 +207,7 @@ VIDATTN_API int vidattn_bwd(const void* q, const void* k, const void* v, const v
   if (plan.kv_split > 1 || plan.q_split > 1) {
     const int64_t n_kv = BH * S_kv * D, n_q = BH * S_q * D;
     const int64_t items = (plan.kv_split > 1 ? n_kv / 2 : 0) + (plan.q_split > 1 ? n_q / 4 : 0);
-    bwd_combine_kernel<0><<<unsigned((items + 255) / 256), 256, 0, stream>>>(
+    bwd_combine_kernel<<<unsigned((items + 255) / 256), 256, 0, stream>>>(
         p.part_kv, plan.kv_split, n_kv, p.part_q, plan.q_split, n_q, scale, p.dk, p.dv, p.dq);
     if (cudaGetLastError() != cudaSuccess) return VIDATTN_ERR_CUDA;
   }

@@ -19,6 +19,12 @@
 // features (so the ring needs no barrier).  Any other N or stride takes the
 // same code with single features, neighbouring lanes on neighbouring ones, and
 // the next rows in registers.
+//
+// Measured (B200): 32760 rows of 5120 bf16 in 125 us (5.4 TB/s, 82 % of the
+// copy rate), backward 218 us (4.6 TB/s); 524160 rows of 128, backward, from a
+// [B,S,H,D] projection 78 us (5.2 TB/s).  Instruction issue bounds it (51 - 64 %
+// of the slots); a deeper ring, one CTA of twice the threads or 32 features a
+// thread were slower.
 #pragma once
 #include <cuda_runtime.h>
 
