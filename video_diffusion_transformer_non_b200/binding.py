@@ -314,28 +314,31 @@ def attention_bwd(dout, q, k, v, out, lse, seg_q=None, seg_kv=None, scale=None, 
     [B,H,S_q].  n_split forces the split of long units (0: the library's
     choice).  Returns bf16 tensors of the shapes of q, k, v; raises on error."""
     import torch
-    _check_qkv(q, k, v)
-    B, H, S_q, D = q.shape
-    S_kv = k.shape[2]
-    _check_tensors(dict(q=q, dout=dout, out=out), torch.bfloat16, ndim=4)
+    _check_tensors(dict(q=q, k=k, v=v, dout=dout, out=out), torch.bfloat16, ndim=4)
     _check_tensors(dict(lse=lse, dlse=dlse), torch.float32, ndim=3)
-    for name, t, shape in (("dout", dout, q.shape), ("out", out, q.shape),
-                           ("lse", lse, q.shape[:3]), ("dlse", dlse, q.shape[:3])):
-        if t is not None and t.shape != shape:
-            raise ValueError(f"{name} must be {tuple(shape)} (is {tuple(t.shape)})")
+    shape = q.shape
+    B, H, S_q, D = shape
+    S_kv = k.shape[2]
+    for name, t, like in (("v", v, k.shape), ("k", k, (B, H, S_kv, D)), ("dout", dout, shape),
+                          ("out", out, shape), ("lse", lse, (B, H, S_q)), ("dlse", dlse, (B, H, S_q))):
+        if t is not None and t.shape != like:
+            raise ValueError(f"{name} must be {tuple(like)} (is {tuple(t.shape)})")
     if lse.device != q.device:
         raise ValueError(f"lse is on {lse.device}, q on {q.device}")
     _check_per_token("seg_q", seg_q, "seg_kv", seg_kv, B, S_q, S_kv, q.device)
     if scale is None:
         scale = D ** -0.5
     flags = (VIDATTN_CAUSAL if causal else 0) | VIDATTN_SPLIT_KV(n_split)
-    n = bwd_workspace(seg_q is not None, B, H, S_q, S_kv, D, flags)
+    n = load_library().vidattn_bwd_workspace(seg_q is not None, B, H, S_q, S_kv, D, flags)
     handle, place = _place(q, stream)
     with place:
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         ws = q.new_empty(max(n, 0), dtype=torch.uint8)
-        st = vidattn_bwd(q, k, v, out, dout, lse, dlse, seg_q, seg_kv, dq, dk, dv, B, H, S_q, S_kv,
-                         D, scale, flags, ws if n > 0 else None, n, handle)
+        st = load_library().vidattn_bwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(),
+            lse.data_ptr(), _ptr(dlse), _ptr(seg_q), _ptr(seg_kv), dq.data_ptr(), dk.data_ptr(),
+            dv.data_ptr(), B, H, S_q, S_kv, D, scale, flags, ws.data_ptr() if n > 0 else None, n,
+            handle)
     if st != VIDATTN_OK:
         raise RuntimeError(f"vidattn_bwd failed: {status_string(st)} ({st})")
     return dq, dk, dv
@@ -389,19 +392,24 @@ def _type_code(t):
 def _rows(name, t, shape=None):
     """A tensor of 1 to 4 dims as rows of [B,H,S,N]: its last dim contiguous,
     any strides for the others.  Returns (B, H, S, N), (sb, sh, ss)."""
-    if not 1 <= t.dim() <= 4:
-        raise ValueError(f"{name} must have 1 to 4 dims (has shape {tuple(t.shape)})")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)} (is {tuple(t.shape)})")
-    if t.stride(-1) != 1 and t.shape[-1] != 1:
+    mine, strides = t.shape, t.stride()
+    if shape is not None and mine != shape:
+        raise ValueError(f"{name} must be {tuple(shape)} (is {tuple(mine)})")
+    dims = len(mine)
+    if not 1 <= dims <= 4:
+        raise ValueError(f"{name} must have 1 to 4 dims (has shape {tuple(mine)})")
+    if strides[-1] != 1 and mine[-1] != 1:
         raise ValueError(f"the last dim of {name} must be contiguous")
-    shape, strides = t.shape, t.stride()
-    if t.dim() < 4:
-        pad = 4 - t.dim()
-        shape, strides = (1,) * pad + tuple(shape), (0,) * pad + strides
-    B, H, S, N = shape
-    return (B, H, S, N), (strides[0] if B > 1 else 0, strides[1] if H > 1 else 0,
-                          strides[2] if S > 1 else 0)
+    if dims < 4:
+        mine, strides = (1,) * (4 - dims) + tuple(mine), (0,) * (4 - dims) + strides
+    B, H, S, N = mine
+    sb, sh, ss, _ = strides
+    return (B, H, S, N), (sb if B > 1 else 0, sh if H > 1 else 0, ss if S > 1 else 0)
+
+
+def _dense(B, H, S, N):
+    """_rows' strides of a contiguous tensor."""
+    return (H * S * N if B > 1 else 0, S * N if H > 1 else 0, N if S > 1 else 0)
 
 
 def _like(t):
@@ -442,13 +450,16 @@ def layer_norm(x, weight=None, bias=None, eps=1e-6, out=None, stream=None):
     (B, H, S, N), sx = _rows("x", x)
     handle, place = _place(x, stream)
     with place:
-        y = _like(x) if out is None else out
-        sy = _rows("out", y, x.shape)[1]
+        if out is None:
+            y, sy = _like(x), _dense(B, H, S, N)
+        else:
+            y, sy = out, _rows("out", out, x.shape)[1]
         mean, rstd = x.new_empty((2, *x.shape[:-1]), dtype=torch.float32).unbind(0)
-        if x.numel() == 0 and N > 0:
+        if N > 0 and B * H * S == 0:
             return y, mean, rstd
-        st = vidattn_layernorm(x, weight, bias, y, mean, rstd, B, H, S, N, sx, sy, x_type, p_type,
-                               eps, handle)
+        st = load_library().vidattn_layernorm(
+            x.data_ptr(), _ptr(weight), _ptr(bias), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+            B, H, S, N, _Strides(*sx), _Strides(*sy), x_type, p_type, eps, handle)
     if st != VIDATTN_OK:
         raise RuntimeError(f"vidattn_layernorm failed: {status_string(st)} ({st})")
     return y, mean, rstd
@@ -470,8 +481,10 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, out=None, stream=None, params
                              f"{tuple(t.shape)} on {t.device})")
     handle, place = _place(x, stream)
     with place:
-        dx = _like(x) if out is None else out
-        sdx = _rows("out", dx, x.shape)[1]
+        if out is None:
+            dx, sdx = _like(x), _dense(B, H, S, N)
+        else:
+            dx, sdx = out, _rows("out", out, x.shape)[1]
         dw = db = ws = None
         n = 0
         if weight is not None and params:
@@ -480,10 +493,12 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, out=None, stream=None, params
                 return dx, dw.zero_(), db.zero_()
             n = layernorm_bwd_workspace(B, H, S, N, x_type)
             ws = x.new_empty(max(n, 0), dtype=torch.uint8)
-        if x.numel() == 0 and N > 0:
+        if N > 0 and B * H * S == 0:
             return dx, None, None
-        st = vidattn_layernorm_bwd(dy, x, mean, rstd, weight, dx, dw, db, B, H, S, N, sdy, sx, sdx,
-                                   x_type, p_type, ws, n, handle)
+        st = load_library().vidattn_layernorm_bwd(
+            dy.data_ptr(), x.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(weight),
+            dx.data_ptr(), _ptr(dw), _ptr(db), B, H, S, N, _Strides(*sdy), _Strides(*sx),
+            _Strides(*sdx), x_type, p_type, _ptr(ws), n, handle)
     if st != VIDATTN_OK:
         raise RuntimeError(f"vidattn_layernorm_bwd failed: {status_string(st)} ({st})")
     return dx, dw, db
@@ -540,6 +555,17 @@ def rope3d(q, k=None, grid=None, bands=None, theta=10000.0, interleaved=True, to
 VIDATTN_ROPE_TRANSPOSE = 2
 
 
+_doubles_types = {}   # length -> ctypes array type (making one costs as much as a launch)
+
+
+def _doubles(values):
+    n = max(len(values), 1)
+    t = _doubles_types.get(n)
+    if t is None:
+        t = _doubles_types[n] = ctypes.c_double * n
+    return t(*values)
+
+
 def vidattn_rope3d_scaled(q_in, k_in, q_out, k_out, B, H, S, D, in_strides, out_strides, T, Hg, Wg,
                           token_offset, d_t, d_h, d_w, freqs, pos_scale, amplitude, flags,
                           stream=None) -> int:
@@ -548,8 +574,8 @@ def vidattn_rope3d_scaled(q_in, k_in, q_out, k_out, B, H, S, D, in_strides, out_
     return load_library().vidattn_rope3d_scaled(
         _ptr(q_in), _ptr(k_in), _ptr(q_out), _ptr(k_out), int(B), int(H), int(S), int(D),
         _strides(in_strides), _strides(out_strides), int(T), int(Hg), int(Wg), int(token_offset),
-        int(d_t), int(d_h), int(d_w), (ctypes.c_double * max(len(freqs), 1))(*freqs),
-        (ctypes.c_double * 3)(*pos_scale), float(amplitude), int(flags), _stream(stream))
+        int(d_t), int(d_h), int(d_w), _doubles(freqs), _doubles(pos_scale), float(amplitude),
+        int(flags), _stream(stream))
 
 
 def _rope_scaled(name, q, k, grid, bands, freqs, pos_scale, amplitude, interleaved, token_offset,
@@ -572,23 +598,27 @@ def _rope_scaled(name, q, k, grid, bands, freqs, pos_scale, amplitude, interleav
     handle, place = _place(q, stream)
     with place:
         if out_q is None:
-            out_q = _like(q)
-        s_out = _rows("out_q", out_q, q.shape)[1]
+            out_q, s_out = _like(q), _dense(B, H, S, D)
+        else:
+            s_out = _rows("out_q", out_q, q.shape)[1]
         if k is not None:
             if out_k is None:
                 out_k = torch.empty_like(out_q)   # of a dense out_q: the same strides
                 if out_k.stride() != out_q.stride():
                     out_k = torch.empty_strided(out_q.shape, out_q.stride(), dtype=k.dtype,
                                                 device=k.device)
-            if _rows("out_k", out_k, q.shape)[1] != s_out:
+            elif _rows("out_k", out_k, q.shape)[1] != s_out:
                 raise ValueError("out_q and out_k must have the same strides")
         if q.numel() == 0 and D > 0:
             return out_q, out_k
         flags = (0 if interleaved else VIDATTN_ROPE_HALF_SPLIT) | \
             (VIDATTN_ROPE_TRANSPOSE if transpose else 0)
-        st = vidattn_rope3d_scaled(q, k, out_q, out_k, B, H, S, D, s_in, s_out, *grid,
-                                   token_offset, *bands, freqs, pos_scale, amplitude, flags,
-                                   handle)
+        T, Hg, Wg = grid
+        d_t, d_h, d_w = bands
+        st = load_library().vidattn_rope3d_scaled(
+            q.data_ptr(), _ptr(k), out_q.data_ptr(), _ptr(out_k), B, H, S, D, _Strides(*s_in),
+            _Strides(*s_out), T, Hg, Wg, token_offset, d_t, d_h, d_w, _doubles(freqs),
+            _doubles(pos_scale), amplitude, flags, handle)
     if st != VIDATTN_OK:
         raise RuntimeError(f"{name} failed: {status_string(st)} ({st})")
     return out_q, out_k
