@@ -32,25 +32,9 @@
 #include <cstdint>
 #include <cuda.h>
 
-#include "fwd_kernel.cuh"
-#include "ptx.cuh"
+#include "ptx_train.cuh"
 
 namespace vidattn {
-
-// 32 lanes x 16 columns, as tmem_ld32.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
-}
 
 constexpr int kBwdSoftmaxWarps = 16;
 constexpr int kBwdMmaWarp = 16, kBwdLoadWarp = 17;
@@ -202,11 +186,30 @@ __device__ __forceinline__ void bwd_issue_acc(uint32_t d_tmem, uint32_t a_tmem, 
   bwd_mma_ts4(d_tmem, a_tmem + 64, b + 512, C::kIdescAcc, 1u);
 }
 
-// warp_wait_phase with its polling loop out of line: the phase has often
-// passed already, and the kernel waits in many places.
+// Bounded wait of a converged warp on an mbarrier phase, with one outcome for
+// all lanes: false if the CTA has aborted, a wait of the launch has timed out
+// or this one does (it then sets the abort flag and the device error word).  The
+// polling is out of line: the phase has often passed already, and the kernel
+// waits in many places.
+constexpr uint64_t kBwdWaitTimeoutNs = 2000000000ull;
+constexpr int kBwdErrTimeout = 1;   // bit of the device error word, as the forward's
 static __device__ __noinline__ bool bwd_wait_slow(uint32_t bar, uint32_t parity,
                                                   volatile int* abort_flag, int* err) {
-  return warp_wait_phase(bar, parity, abort_flag, err);
+  uint64_t t0 = 0;
+  bool ok = mbar_try_wait(bar, parity);
+  for (uint32_t it = 1; !ok; ++it) {
+    ok = mbar_try_wait(bar, parity);
+    if (ok || (it & 255u) != 0) continue;
+    // give up at once if this CTA, or any CTA of this launch, already did
+    const bool gone = *abort_flag != 0 || *reinterpret_cast<volatile int*>(err) != 0;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (!gone && now - t0 <= kBwdWaitTimeoutNs) continue;
+    *abort_flag = 1;
+    if (!gone) atomicOr(err, kBwdErrTimeout);
+    break;
+  }
+  return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ bool bwd_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                          int* err) {
@@ -241,21 +244,6 @@ __device__ __forceinline__ void bulk_load_elect(uint32_t dst, const void* src, u
       "\n\t}\n" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
       : "memory");
-}
-
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
-                                             uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
-               "r"(d)
-               : "memory");
-}
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
 }
 
 // The other-side tiles a unit walks: positions [t0, t1) of its visit sequence,
@@ -549,7 +537,7 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
     for (int n = 1, pos = n_tiles > 0 ? walk.next(walk.start) + 1 : 0; n < n_tiles && ok; ++n, ++pos) {
       pos = walk.next(pos);
       for (int which = 0; which < 2 && ok; ++which) {
-        ok = warp_wait_phase(which ? b_empty(n) : a_empty(n), (which ? b_par(n) : a_par(n)) ^ 1u,
+        ok = bwd_wait(which ? b_empty(n) : a_empty(n), (which ? b_par(n) : a_par(n)) ^ 1u,
                              abort_flag, p.err);
         if (ok) load(n, walk.first + pos, which);
       }
@@ -559,11 +547,11 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
       // the phase of its load, or by its time limit)
       volatile int never = 0;
       for (int k = max(0, n_a - kA); k < n_a; ++k)
-        warp_wait_phase(a_full(k), a_par(k), &never, p.err);
+        bwd_wait_slow(a_full(k), a_par(k), &never, p.err);
       for (int k = max(0, n_b - kB); k < n_b; ++k)
-        warp_wait_phase(b_full(k), b_par(k), &never, p.err);
+        bwd_wait_slow(b_full(k), b_par(k), &never, p.err);
       for (int which = 0; which < 2; ++which)
-        warp_wait_phase(fixed_full(which), 0, &never, p.err);
+        bwd_wait_slow(fixed_full(which), 0, &never, p.err);
     }
     __syncwarp();
   } else if (warp == kBwdMmaWarp) {
@@ -626,7 +614,7 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
     // of tensor memory
     mma_commit_elect(done);
     volatile int never = 0;
-    warp_wait_phase(done, 0, &never, p.err);
+    bwd_wait_slow(done, 0, &never, p.err);
     __syncwarp();
   } else if (warp < kBwdSoftmaxWarps) {
     // --------------------------------------------------------- P and dS
@@ -726,7 +714,7 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
       arrive(ds_full(n));
     }
     // ------------------------------------------------------------ epilogue
-    ok = ok && warp_wait_phase(done, 0, abort_flag, p.err);
+    ok = ok && bwd_wait_slow(done, 0, abort_flag, p.err);
     if (ok) {
       tc_fence_after();
       // every load and product is over: the rings are free to stage the stores
@@ -775,7 +763,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // a wait of an earlier CTA timed out: the results are already invalid
   if (*reinterpret_cast<volatile int*>(p.err) != 0) return;
   if (sbase & 1023u) {   // the tiles' swizzle needs the alignment asked for above
-    if (threadIdx.x == 0) atomicOr(p.err, kErrTimeout);
+    if (threadIdx.x == 0) atomicOr(p.err, kBwdErrTimeout);
     return;
   }
 

@@ -376,7 +376,7 @@ __device__ __forceinline__ uint4 tile_mask(const int32_t* kinfo, int mode, int m
 
 // The same as a call, so that its registers do not weigh on the softmax's
 // where masked tiles are rare.
-static __device__ __noinline__ uint4 tile_mask_call(const int32_t* kinfo, int mode, int my_seg, int ws0,
+__device__ __noinline__ uint4 tile_mask_call(const int32_t* kinfo, int mode, int my_seg, int ws0,
                                              int ws1, int ws2, int k0, int k1, int k2,
                                              int n_lim) {
   return tile_mask(kinfo, mode, my_seg, ws0, ws1, ws2, k0, k1, k2, n_lim);

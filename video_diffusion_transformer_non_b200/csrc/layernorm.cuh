@@ -30,7 +30,7 @@
 
 #include <cstdint>
 
-#include "ptx.cuh"
+#include "ptx_train.cuh"
 
 namespace vidattn {
 
