@@ -82,6 +82,9 @@ __host__ __device__ constexpr int ln_stages(int threads, int rows, int tensors, 
 __device__ __forceinline__ void ln_copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void ln_copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void ln_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kPending>
 __device__ __forceinline__ void ln_wait() {
@@ -431,6 +434,14 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_bwd_kernel(const LnPara
 #pragma unroll
   for (int e = 0; e < kE / 2; ++e) dw[e] = db[e] = ln_both(0.f);
   Frag nx[kRing ? 1 : kR], ng[kRing ? 1 : kR];
+  // the rows' statistics travel in the ring too, a copy for every warp (or group
+  // of lanes): read from memory by all its threads, a turn ahead, they held up
+  // the rows (long scoreboard stalls, 219 against 186 us without them)
+  constexpr int kOwners = kBlock ? 32 : kLnThreads / (kBlock ? 1 : kLanes);
+  __shared__ float2 stats[kRing ? kS : 1][kR][kOwners];
+  const int owner = kBlock ? threadIdx.x >> 5 : t.group;
+  const int owner_lane = kBlock ? threadIdx.x & 31 : lane;
+  int st_in = 0, st_out = 0;
   float nm[kR], nr[kR];
   auto fetch = [&](uint32_t row0) {
 #pragma unroll
@@ -442,6 +453,9 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_bwd_kernel(const LnPara
                      t.valid);
           Frag::copy(t.slot(t.in, i, 1), t.pitch, dy + ln_offset(p, p.ldy, row), lane, lanes,
                      t.valid);
+          if (owner_lane < 2)
+            ln_copy4(smem_u32(&stats[st_in][i][owner]) + 4 * owner_lane,
+                     (owner_lane ? p.rstd : p.mean) + row);
         }
       } else if (row < p.rows) {
         nx[i].load(x + ln_offset(p, p.lx, row), lane, lanes, p.N);
@@ -453,6 +467,7 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_bwd_kernel(const LnPara
     }
     if constexpr (kRing) {
       t.next(t.in);
+      st_in = st_in + 1 == kS ? 0 : st_in + 1;
       ln_commit();
     }
   };
@@ -467,7 +482,7 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_bwd_kernel(const LnPara
       }
     }
   };
-  fetch_stats(t.row);
+  if constexpr (!kRing) fetch_stats(t.row);
   if constexpr (kRing) {
 #pragma unroll
     for (int k = 0; k < kS - 1; ++k) fetch(t.row + k * t.step);
@@ -478,19 +493,28 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_bwd_kernel(const LnPara
   for (int turn = 0; t.any(p); turn ^= 1, t.row += t.step) {
     Frag cx[kR], cg[kR];
     float m[kR], r[kR], c[2 * kR];
+    if constexpr (!kRing) {
 #pragma unroll
-    for (int i = 0; i < kR; ++i) m[i] = -nm[i], r[i] = nr[i];
-    fetch_stats(t.row + t.step);
+      for (int i = 0; i < kR; ++i) m[i] = -nm[i], r[i] = nr[i];
+      fetch_stats(t.row + t.step);
+    }
     if constexpr (kRing) {
       fetch(t.row + (kS - 1) * t.step);
       ln_wait<kRing ? kS - 1 : 0>();
+      __syncwarp();   // the statistics came by two of the lanes
 #pragma unroll
       for (int i = 0; i < kR; ++i) {
+        const float2 st = stats[st_out][i][owner];
+        m[i] = -st.x, r[i] = st.y;
         cx[i].read(t.slot(t.out, i, 0), t.pitch, t.valid);
         cg[i].read(t.slot(t.out, i, 1), t.pitch, t.valid);
-        if (t.row + i * t.groups >= p.rows) cx[i].clear(), cg[i].clear();   // no row: no share
+        if (t.row + i * t.groups >= p.rows) {   // no row: no share
+          cx[i].clear(), cg[i].clear();
+          m[i] = r[i] = 0.f;
+        }
       }
       t.next(t.out);
+      st_out = st_out + 1 == kS ? 0 : st_out + 1;
     } else {
 #pragma unroll
       for (int i = 0; i < kR; ++i) cx[i] = nx[i], cg[i] = ng[i];
