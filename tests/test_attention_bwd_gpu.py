@@ -161,7 +161,7 @@ def test_joint_sequence():
 
 
 def test_more_tiles_than_a_unit_lists():
-    """With ids and more query tiles than a unit keeps as bits (3072), it walks
+    """With ids and more query tiles than a unit keeps as bits, it walks
     every tile of its range and masks them all."""
     S_q = 3100 * 128 + 5
     x = make(1, 1, S_q, 200, 64, 7500, "runs")

@@ -39,7 +39,7 @@ namespace vidattn {
 constexpr int kBwdSoftmaxWarps = 16;
 constexpr int kBwdMmaWarp = 16, kBwdLoadWarp = 17;
 constexpr int kBwdThreads = 640;   // 2 warps more: registers are dealt to 4 warps at a time
-constexpr int kBwdMaxListed = 3072;   // tiles of a unit's range whose visits are kept as bits
+constexpr int kBwdMaxListed = 2944;   // tiles of a unit's range whose visits are kept as bits
 
 struct BwdParams {
   // per 128-row query tile: -lse * log2(e) (row sees nothing or is past S_q:
