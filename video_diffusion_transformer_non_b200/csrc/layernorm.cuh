@@ -12,13 +12,13 @@
 // workspace and are added by a second kernel in a fixed order.
 //
 // Rows of up to 1024 features belong to 8, 16 or 32 lanes of a warp (no
-// barrier); longer ones to a CTA with 16 features a thread.  What bounds the pass
-// is how many bytes are in flight: rows that lie on 16-byte boundaries with N
-// a multiple of 8 go through a ring in shared memory, filled by cp.async up to
-// three turns ahead, each thread copying and reading its own 8 neighbouring
-// features (so the ring needs no barrier).  Any other N or stride takes the
-// same code with single features, neighbouring lanes on neighbouring ones, and
-// the next rows in registers.
+// barrier); longer ones to a CTA with 16 features a thread.  What bounds the
+// pass is how many bytes are in flight: rows go through a ring in shared memory,
+// filled by cp.async up to three turns ahead, each thread copying and reading its
+// own features (so the ring needs no barrier).  Rows on 16-byte boundaries with
+// N a multiple of 16 bytes move in pieces of 16 bytes, the others in pieces of 4;
+// bf16 rows on odd places or of odd length, which cp.async cannot copy, go
+// feature by feature through registers.
 //
 // Measured (B200): 32760 rows of 5120 bf16 in 125 us (5.4 TB/s, 82 % of the
 // copy rate), backward 218 us (4.6 TB/s); 524160 rows of 128, backward, from a
@@ -91,18 +91,25 @@ __device__ __forceinline__ void ln_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
-// kC chunks of 8 features of one row, as read: X is float or uint16_t (bf16).
-template <typename X, int kC, bool kVec>
+// The row's feature that element e of a lane is: pieces of kV neighbouring
+// features, neighbouring lanes on neighbouring pieces.
+template <int kV>
+__device__ __forceinline__ int ln_col(int e, int lane, int lanes) {
+  return ((e / kV) * lanes + lane) * kV + e % kV;
+}
+
+// 8 kC features of one row, as read: X is float or uint16_t (bf16), in pieces
+// of kV (16 or 4 bytes; 2 for bf16 rows on odd places).  N is a multiple of kV.
+template <typename X, int kC, int kV>
 struct LnFrag {
   static constexpr int kE = 8 * kC;
-  static constexpr bool kBf16 = sizeof(X) == 2;
-  static constexpr int kWords = kVec && kBf16 ? 4 * kC : kE;
+  static constexpr int kPieces = kE / kV;
+  static constexpr int kPieceBytes = kV * int(sizeof(X));
+  static constexpr bool kAsync = kPieceBytes >= 4;   // by cp.async
+  static constexpr bool kPacked = sizeof(X) == 2 && kAsync;
+  static constexpr int kWords = kPacked ? kE / 2 : kE;
   uint32_t r[kWords];
 
-  // The row's feature that element e of this lane is.
-  static __device__ __forceinline__ int col(int e, int lane, int lanes) {
-    return kVec ? ((e >> 3) * lanes + lane) * 8 + (e & 7) : e * lanes + lane;
-  }
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) r[i] = 0u;
@@ -110,62 +117,55 @@ struct LnFrag {
   // Features at and behind N read as 0.
   __device__ __forceinline__ void load(const X* row, int lane, int lanes, int N) {
     clear();
-    if constexpr (kVec) {
-#pragma unroll
-      for (int c = 0; c < kC; ++c) {
-        const int at = (c * lanes + lane) * 8;
-        if (at < N) {
-#pragma unroll
-          for (int k = 0; k < kWords / kC / 4; ++k) {
-            const uint4 v = *reinterpret_cast<const uint4*>(
-                reinterpret_cast<const char*>(row + at) + 16 * k);
-            uint32_t* d = r + c * (kWords / kC) + 4 * k;
-            d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
-          }
-        }
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        const int at = e * lanes + lane;
-        if (at < N) {
-          if constexpr (kBf16) r[e] = uint32_t(row[at]) << 16;
-          else r[e] = __float_as_uint(row[at]);
-        }
-      }
-    }
-  }
-  // The same by way of shared memory: kPieces pieces of 16 bytes a thread, at
-  // `ring` (a shared address of this thread's) and every `pitch` bytes from
-  // there.  valid: which chunks begin in front of N.
-  static constexpr int kPieces = kWords / 4;
-  static __device__ __forceinline__ void copy(uint32_t ring, uint32_t pitch, const X* row,
-                                              int lane, int lanes, const bool (&valid)[kC]) {
-#pragma unroll
-    for (int c = 0; c < kC; ++c) {
-      if (valid[c]) {
-#pragma unroll
-        for (int k = 0; k < kPieces / kC; ++k)
-          ln_copy16(ring + (c * (kPieces / kC) + k) * pitch,
-                    reinterpret_cast<const char*>(row + (c * lanes + lane) * 8) + 16 * k);
-      }
-    }
-  }
-  __device__ __forceinline__ void read(uint32_t ring, uint32_t pitch, const bool (&valid)[kC]) {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      uint32_t* d = r + 4 * i;
-      d[0] = d[1] = d[2] = d[3] = 0u;
-      if (valid[i / (kPieces / kC)])
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
-                     : "r"(ring + i * pitch)
-                     : "memory");
+      const int at = (i * lanes + lane) * kV;
+      if (at >= N) continue;
+      uint32_t* d = r + i * (kWords / kPieces);
+      if constexpr (kPieceBytes == 16) {
+        const uint4 v = *reinterpret_cast<const uint4*>(row + at);
+        d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
+      } else if constexpr (kPieceBytes == 4) {
+        d[0] = *reinterpret_cast<const uint32_t*>(row + at);
+      } else {
+        d[0] = uint32_t(row[at]) << 16;
+      }
+    }
+  }
+  // The same by way of shared memory: a piece every `pitch` bytes from `ring`,
+  // a shared address of this thread's.
+  static __device__ __forceinline__ void copy(uint32_t ring, uint32_t pitch, const X* row,
+                                              int lane, int lanes, int N) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int at = (i * lanes + lane) * kV;
+      if (at >= N) continue;
+      if constexpr (kPieceBytes == 16) ln_copy16(ring + i * pitch, row + at);
+      else ln_copy4(ring + i * pitch, row + at);
+    }
+  }
+  __device__ __forceinline__ void read(uint32_t ring, uint32_t pitch, int lane, int lanes, int N) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const bool in = (i * lanes + lane) * kV < N;
+      uint32_t* d = r + i * (kWords / kPieces);
+      if constexpr (kPieceBytes == 16) {
+        d[0] = d[1] = d[2] = d[3] = 0u;
+        if (in)
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+                       : "r"(ring + i * pitch)
+                       : "memory");
+      } else {
+        d[0] = 0u;
+        if (in)
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(d[0]) : "r"(ring + i * pitch) : "memory");
+      }
     }
   }
   // Elements 2 i and 2 i + 1.
   __device__ __forceinline__ float2 get2(int i) const {
-    if constexpr (kVec && kBf16)
+    if constexpr (kPacked)
       return make_float2(__uint_as_float(r[i] << 16), __uint_as_float(r[i] & 0xffff0000u));
     else
       return make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
@@ -173,46 +173,39 @@ struct LnFrag {
 };
 __device__ __forceinline__ float2 ln_both(float v) { return make_float2(v, v); }
 
-template <typename X, int kC, bool kVec>
+template <typename X, int kC, int kV>
 __device__ __forceinline__ void ln_store(X* row, int lane, int lanes, int N,
                                          const float2 (&v)[4 * kC]) {
-  if constexpr (kVec) {
 #pragma unroll
-    for (int c = 0; c < kC; ++c) {
-      const int at = (c * lanes + lane) * 8;
-      if (at >= N) continue;
-      const float2* s = v + 4 * c;
-      if constexpr (sizeof(X) == 2) {
+  for (int i = 0; i < 8 * kC / kV; ++i) {
+    const int at = (i * lanes + lane) * kV;
+    if (at >= N) continue;
+    if constexpr (kV >= 2) {
+      const float2* s = v + i * (kV / 2);
+      if constexpr (sizeof(X) == 4)
+        *reinterpret_cast<float4*>(row + at) = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
+      else if constexpr (kV == 8)
         *reinterpret_cast<uint4*>(row + at) =
             make_uint4(pack_bf16x2(s[0].x, s[0].y), pack_bf16x2(s[1].x, s[1].y),
                        pack_bf16x2(s[2].x, s[2].y), pack_bf16x2(s[3].x, s[3].y));
-      } else {
-        float4* d = reinterpret_cast<float4*>(row + at);
-        d[0] = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
-        d[1] = make_float4(s[2].x, s[2].y, s[3].x, s[3].y);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8 * kC; ++e) {
-      const int at = e * lanes + lane;
-      if (at < N) {
-        const float t = (e & 1) ? v[e / 2].y : v[e / 2].x;
-        if constexpr (sizeof(X) == 2) row[at] = ln_to_bf16(t);
-        else row[at] = t;
-      }
+      else
+        *reinterpret_cast<uint32_t*>(row + at) = pack_bf16x2(s[0].x, s[0].y);
+    } else {
+      const float t = (i & 1) ? v[i / 2].y : v[i / 2].x;
+      if constexpr (sizeof(X) == 2) row[at] = ln_to_bf16(t);
+      else row[at] = t;
     }
   }
 }
 
 // This thread's features of weight or bias (null: `none`).
-template <typename P, int kC, bool kVec>
+template <typename P, int kC, int kV>
 __device__ __forceinline__ void ln_params_of(const P* src, int lane, int lanes, int N,
                                              float2 (&v)[4 * kC]) {
   P t[8 * kC];
 #pragma unroll
   for (int e = 0; e < 8 * kC; ++e) {
-    const int at = LnFrag<float, kC, kVec>::col(e, lane, lanes);
+    const int at = ln_col<kV>(e, lane, lanes);
     t[e] = at < N ? __ldg(src + at) : P(0);
   }
 #pragma unroll
@@ -221,16 +214,16 @@ __device__ __forceinline__ void ln_params_of(const P* src, int lane, int lanes, 
     else v[e] = make_float2(t[2 * e], t[2 * e + 1]);
   }
 }
-template <int kC, bool kVec>
+template <int kC, int kV>
 __device__ __forceinline__ void ln_params(const void* src, int bf16, int lane, int lanes, int N,
                                           float none, float2 (&v)[4 * kC]) {
   if (src == nullptr) {
 #pragma unroll
     for (int e = 0; e < 4 * kC; ++e) v[e] = ln_both(none);
   } else if (bf16) {
-    ln_params_of<uint16_t, kC, kVec>(static_cast<const uint16_t*>(src), lane, lanes, N, v);
+    ln_params_of<uint16_t, kC, kV>(static_cast<const uint16_t*>(src), lane, lanes, N, v);
   } else {
-    ln_params_of<float, kC, kVec>(static_cast<const float*>(src), lane, lanes, N, v);
+    ln_params_of<float, kC, kV>(static_cast<const float*>(src), lane, lanes, N, v);
   }
   // kept in registers, not read again for every row
 #pragma unroll
@@ -272,15 +265,14 @@ extern __shared__ uint4 ln_ring[];
 // What both kernels share: the rows a thread works on, kR at a time (kBlock:
 // the CTA's kR next rows; else every group of kLanes threads has a row of its
 // own in each of kR turns), its features, and the ring.
-template <typename X, int kLanes, int kC, int kR, bool kVec, int kMaxThreads, int kTensors>
+template <typename X, int kLanes, int kC, int kR, int kV, int kMaxThreads, int kTensors>
 struct LnWalk {
   static constexpr bool kBlock = kLanes == 0;
-  using Frag = LnFrag<X, kC, kVec>;
-  static constexpr int kS = kVec ? ln_stages(kMaxThreads, kR, kTensors, Frag::kWords * 4) : 0;
+  using Frag = LnFrag<X, kC, kV>;
+  static constexpr int kS = Frag::kAsync ? ln_stages(kMaxThreads, kR, kTensors, Frag::kWords * 4) : 0;
   static constexpr bool kRing = kS >= 2;
   int lanes, lane, groups, group;
   uint32_t row, step, pitch, stage, ring, in, out;   // in, out: ring addresses of this thread's
-  bool valid[kC];
   __device__ __forceinline__ explicit LnWalk(const LnParams& p) {
     lanes = kBlock ? blockDim.x : kLanes;
     lane = kBlock ? threadIdx.x : threadIdx.x % (kBlock ? 1 : kLanes);
@@ -288,17 +280,15 @@ struct LnWalk {
     groups = kBlock ? 1 : kLnThreads / (kBlock ? 1 : kLanes);
     row = blockIdx.x * groups * kR + group;
     step = gridDim.x * groups * kR;
-    pitch = blockDim.x * 16;
-    stage = pitch * Frag::kWords / 4 * kTensors * kR;
-    ring = smem_u32(ln_ring) + threadIdx.x * 16;
+    pitch = blockDim.x * Frag::kPieceBytes;
+    stage = pitch * Frag::kPieces * kTensors * kR;
+    ring = smem_u32(ln_ring) + threadIdx.x * Frag::kPieceBytes;
     in = out = ring;
-#pragma unroll
-    for (int c = 0; c < kC; ++c) valid[c] = (c * lanes + lane) * 8 < p.N;
   }
   // the CTA's first row of this turn decides whether the turn is made at all
   __device__ __forceinline__ bool any(const LnParams& p) const { return row - group < p.rows; }
   __device__ __forceinline__ uint32_t slot(uint32_t at, int i, int tensor) const {
-    return at + (i * kTensors + tensor) * (Frag::kWords / 4) * pitch;
+    return at + (i * kTensors + tensor) * Frag::kPieces * pitch;
   }
   __device__ __forceinline__ void next(uint32_t& at) const {
     at += stage;
@@ -306,9 +296,9 @@ struct LnWalk {
   }
 };
 
-template <typename X, int kLanes, int kC, int kR, bool kVec, int kMaxThreads, int kCtas>
+template <typename X, int kLanes, int kC, int kR, int kV, int kMaxThreads, int kCtas>
 __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_fwd_kernel(const LnParams p) {
-  using Walk = LnWalk<X, kLanes, kC, kR, kVec, kMaxThreads, 1>;
+  using Walk = LnWalk<X, kLanes, kC, kR, kV, kMaxThreads, 1>;
   using Frag = typename Walk::Frag;
   constexpr bool kBlock = Walk::kBlock, kRing = Walk::kRing;
   constexpr int kE = 8 * kC, kS = Walk::kS;
@@ -329,7 +319,7 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_fwd_kernel(const LnPara
       if constexpr (kRing) {
         if (row < p.rows)
           Frag::copy(t.slot(t.in, i, 0), t.pitch, x + ln_offset(p, p.lx, row), lane, lanes,
-                     t.valid);
+                     p.N);
       } else {
         if (row < p.rows) next[i].load(x + ln_offset(p, p.lx, row), lane, lanes, p.N);
         else next[i].clear();
@@ -347,15 +337,15 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_fwd_kernel(const LnPara
     fetch(t.row);
   }
   float2 w[kE / 2], b[kE / 2];
-  ln_params<kC, kVec>(p.w, p.params_bf16, lane, lanes, p.N, 1.f, w);
-  ln_params<kC, kVec>(p.b, p.params_bf16, lane, lanes, p.N, 0.f, b);
+  ln_params<kC, kV>(p.w, p.params_bf16, lane, lanes, p.N, 1.f, w);
+  ln_params<kC, kV>(p.b, p.params_bf16, lane, lanes, p.N, 0.f, b);
   for (int turn = 0; t.any(p); turn ^= 1, t.row += t.step) {
     Frag cur[kR];
     if constexpr (kRing) {
       fetch(t.row + (kS - 1) * t.step);
       ln_wait<kRing ? kS - 1 : 0>();
 #pragma unroll
-      for (int i = 0; i < kR; ++i) cur[i].read(t.slot(t.out, i, 0), t.pitch, t.valid);
+      for (int i = 0; i < kR; ++i) cur[i].read(t.slot(t.out, i, 0), t.pitch, lane, lanes, p.N);
       t.next(t.out);
     } else {
 #pragma unroll
@@ -382,11 +372,11 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_fwd_kernel(const LnPara
 #pragma unroll
       for (int e = 0; e < kE / 2; ++e) {
         d[i][e] = fadd2(d[i][e], ln_both(-mean[i]));
-        if (kVec) {   // features behind N add nothing
-          if (t.valid[e / 4]) s = ffma2(d[i][e], d[i][e], s);
+        if (kV >= 2) {   // features behind N add nothing
+          if (ln_col<kV>(2 * e, lane, lanes) < p.N) s = ffma2(d[i][e], d[i][e], s);
         } else {
-          if (Frag::col(2 * e, lane, lanes) < p.N) s.x = fmaf(d[i][e].x, d[i][e].x, s.x);
-          if (Frag::col(2 * e + 1, lane, lanes) < p.N) s.y = fmaf(d[i][e].y, d[i][e].y, s.y);
+          if (ln_col<kV>(2 * e, lane, lanes) < p.N) s.x = fmaf(d[i][e].x, d[i][e].x, s.x);
+          if (ln_col<kV>(2 * e + 1, lane, lanes) < p.N) s.y = fmaf(d[i][e].y, d[i][e].y, s.y);
         }
       }
       var[i] = s.x + s.y;
@@ -399,7 +389,7 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_fwd_kernel(const LnPara
       if (row < p.rows) {
 #pragma unroll
         for (int e = 0; e < kE / 2; ++e) d[i][e] = ffma2(fmul2(d[i][e], ln_both(rstd)), w[e], b[e]);
-        ln_store<X, kC, kVec>(y + ln_offset(p, p.ly, row), lane, lanes, p.N, d[i]);
+        ln_store<X, kC, kV>(y + ln_offset(p, p.ly, row), lane, lanes, p.N, d[i]);
         if (lane == 0) {
           if (p.mean) p.mean[row] = mean[i];
           if (p.rstd) p.rstd[row] = rstd;
@@ -410,9 +400,9 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_fwd_kernel(const LnPara
   }
 }
 
-template <typename X, int kLanes, int kC, int kR, bool kVec, int kMaxThreads, int kCtas>
+template <typename X, int kLanes, int kC, int kR, int kV, int kMaxThreads, int kCtas>
 __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_bwd_kernel(const LnParams p) {
-  using Walk = LnWalk<X, kLanes, kC, kR, kVec, kMaxThreads, 2>;
+  using Walk = LnWalk<X, kLanes, kC, kR, kV, kMaxThreads, 2>;
   using Frag = typename Walk::Frag;
   constexpr bool kBlock = Walk::kBlock, kRing = Walk::kRing;
   constexpr int kE = 8 * kC, kS = Walk::kS;
@@ -450,9 +440,9 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_bwd_kernel(const LnPara
       if constexpr (kRing) {
         if (row < p.rows) {
           Frag::copy(t.slot(t.in, i, 0), t.pitch, x + ln_offset(p, p.lx, row), lane, lanes,
-                     t.valid);
+                     p.N);
           Frag::copy(t.slot(t.in, i, 1), t.pitch, dy + ln_offset(p, p.ldy, row), lane, lanes,
-                     t.valid);
+                     p.N);
           if (owner_lane < 2)
             ln_copy4(smem_u32(&stats[st_in][i][owner]) + 4 * owner_lane,
                      (owner_lane ? p.rstd : p.mean) + row);
@@ -489,7 +479,7 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_bwd_kernel(const LnPara
   } else {
     fetch(t.row);
   }
-  ln_params<kC, kVec>(p.w, p.params_bf16, lane, lanes, p.N, 1.f, w);
+  ln_params<kC, kV>(p.w, p.params_bf16, lane, lanes, p.N, 1.f, w);
   for (int turn = 0; t.any(p); turn ^= 1, t.row += t.step) {
     Frag cx[kR], cg[kR];
     float m[kR], r[kR], c[2 * kR];
@@ -506,8 +496,8 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_bwd_kernel(const LnPara
       for (int i = 0; i < kR; ++i) {
         const float2 st = stats[st_out][i][owner];
         m[i] = -st.x, r[i] = st.y;
-        cx[i].read(t.slot(t.out, i, 0), t.pitch, t.valid);
-        cg[i].read(t.slot(t.out, i, 1), t.pitch, t.valid);
+        cx[i].read(t.slot(t.out, i, 0), t.pitch, lane, lanes, p.N);
+        cg[i].read(t.slot(t.out, i, 1), t.pitch, lane, lanes, p.N);
         if (t.row + i * t.groups >= p.rows) {   // no row: no share
           cx[i].clear(), cg[i].clear();
           m[i] = r[i] = 0.f;
@@ -553,7 +543,7 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_bwd_kernel(const LnPara
           const float2 gw = kKeep ? kg[kKeep ? i : 0][kKeep ? e : 0] : fmul2(cg[i].get2(e), w[e]);
           v[e] = ffma2(xh, c2, ffma2(gw, ln_both(r[i]), c1));
         }
-        ln_store<X, kC, kVec>(dx + ln_offset(p, p.ly, row), lane, lanes, p.N, v);
+        ln_store<X, kC, kV>(dx + ln_offset(p, p.ly, row), lane, lanes, p.N, v);
       }
     }
     if (!kRing && !kBlock) fetch(t.row + t.step);
@@ -565,7 +555,7 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_bwd_kernel(const LnPara
   if constexpr (kBlock) {
 #pragma unroll
     for (int e = 0; e < kE; ++e) {
-      const int at = Frag::col(e, lane, lanes);
+      const int at = ln_col<kV>(e, lane, lanes);
       if (at < p.N) {
         part[at] = value(dw, e);
         part[p.N + at] = value(db, e);
@@ -587,7 +577,7 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_bwd_kernel(const LnPara
         float t = 0.f;
 #pragma unroll
         for (int k = 0; k < kLnThreads / 32; ++k) t += sums[k][i];
-        const int at = Frag::col(i / kLanes, i % kLanes, kLanes);
+        const int at = ln_col<kV>(i / kLanes, i % kLanes, kLanes);
         if (at < p.N) part[which * p.N + at] = t;
       }
       __syncthreads();

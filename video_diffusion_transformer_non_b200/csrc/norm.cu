@@ -31,33 +31,36 @@ struct LnChoice {
 // kLanes of a warp a row (0: the CTA), kC chunks of 8 features a thread, kR
 // rows a thread at a time; registers for kFwd (kBwd) CTAs on an SM: the reductions
 // leave a CTA idle, the next one fills in.
-template <typename X, int kLanes, int kC, int kR, bool kVec, int kMaxThreads, int kFwd, int kBwd>
+template <typename X, int kLanes, int kC, int kR, int kV, int kMaxThreads, int kFwd, int kBwd>
 LnChoice ln_form(bool bwd, int threads) {
-  const int piece = LnFrag<X, kC, kVec>::kWords * 4, tensors = bwd ? 2 : 1;
-  const int stages = kVec ? ln_stages(kMaxThreads, kR, tensors, piece) : 0;
-  return LnChoice{bwd ? ln_bwd_kernel<X, kLanes, kC, kR, kVec, kMaxThreads, kBwd>
-                      : ln_fwd_kernel<X, kLanes, kC, kR, kVec, kMaxThreads, kFwd>,
+  using Frag = LnFrag<X, kC, kV>;
+  const int piece = Frag::kWords * 4, tensors = bwd ? 2 : 1;
+  const int stages = Frag::kAsync ? ln_stages(kMaxThreads, kR, tensors, piece) : 0;
+  return LnChoice{bwd ? ln_bwd_kernel<X, kLanes, kC, kR, kV, kMaxThreads, kBwd>
+                      : ln_fwd_kernel<X, kLanes, kC, kR, kV, kMaxThreads, kFwd>,
                   threads, kLanes ? threads / kLanes * kR : kR,
                   stages >= 2 ? stages * threads * kR * tensors * piece : 0,
                   stages >= 2 ? stages * kMaxThreads * kR * tensors * piece : 0};
 }
 
 // The smallest form that holds a row of N features in registers.
-template <typename X, bool kVec>
+template <typename X, int kV>
 LnChoice ln_choose_x(bool bwd, int N) {
-  if (N <= 64) return ln_form<X, 8, 1, 2, kVec, kLnThreads, 3, 2>(bwd, kLnThreads);
-  if (N <= 128) return ln_form<X, 16, 1, 2, kVec, kLnThreads, 3, 2>(bwd, kLnThreads);
-  if (N <= 256) return ln_form<X, 32, 1, 2, kVec, kLnThreads, 3, 2>(bwd, kLnThreads);
-  if (N <= 512) return ln_form<X, 32, 2, 1, kVec, kLnThreads, 2, 2>(bwd, kLnThreads);
-  if (N <= 1024) return ln_form<X, 32, 4, 1, kVec, kLnThreads, 1, 1>(bwd, kLnThreads);
+  if (N <= 64) return ln_form<X, 8, 1, 2, kV, kLnThreads, 3, 2>(bwd, kLnThreads);
+  if (N <= 128) return ln_form<X, 16, 1, 2, kV, kLnThreads, 3, 2>(bwd, kLnThreads);
+  if (N <= 256) return ln_form<X, 32, 1, 2, kV, kLnThreads, 3, 2>(bwd, kLnThreads);
+  if (N <= 512) return ln_form<X, 32, 2, 1, kV, kLnThreads, 2, 2>(bwd, kLnThreads);
+  if (N <= 1024) return ln_form<X, 32, 4, 1, kV, kLnThreads, 1, 1>(bwd, kLnThreads);
   const int threads = (N + 511) / 512 * 32;
-  if (threads <= 320) return ln_form<X, 0, 2, 1, kVec, 320, 2, 2>(bwd, threads);
-  if (threads <= 512) return ln_form<X, 0, 2, 1, kVec, 512, 1, 1>(bwd, threads);
-  return ln_form<X, 0, 2, 1, kVec, 1024, 1, 1>(bwd, threads);
+  if (threads <= 320) return ln_form<X, 0, 2, 1, kV, 320, 2, 2>(bwd, threads);
+  if (threads <= 512) return ln_form<X, 0, 2, 1, kV, 512, 1, 1>(bwd, threads);
+  return ln_form<X, 0, 2, 1, kV, 1024, 1, 1>(bwd, threads);
 }
-LnChoice ln_choose(bool bwd, bool bf16, bool vec, int N) {
-  if (bf16) return vec ? ln_choose_x<uint16_t, true>(bwd, N) : ln_choose_x<uint16_t, false>(bwd, N);
-  return vec ? ln_choose_x<float, true>(bwd, N) : ln_choose_x<float, false>(bwd, N);
+// piece: 16, 4 or 2, the bytes that every row's start and length are a multiple of.
+LnChoice ln_choose(bool bwd, bool bf16, int piece, int N) {
+  if (!bf16) return piece == 16 ? ln_choose_x<float, 4>(bwd, N) : ln_choose_x<float, 1>(bwd, N);
+  if (piece == 16) return ln_choose_x<uint16_t, 8>(bwd, N);
+  return piece == 4 ? ln_choose_x<uint16_t, 2>(bwd, N) : ln_choose_x<uint16_t, 1>(bwd, N);
 }
 
 // CTAs of a launch: enough for all rows, at most what the device holds at once
@@ -100,9 +103,9 @@ bool ln_apart(int B, int H, int S, int N, const int64_t s[3]) {
 }
 // Any read layout: strides not negative.
 bool ln_readable(const int64_t s[3]) { return s[0] >= 0 && s[1] >= 0 && s[2] >= 0; }
-bool ln_vector(const void* p, const int64_t s[3], int item) {
-  return host::aligned(p, 16) && s[0] * item % 16 == 0 && s[1] * item % 16 == 0 &&
-         s[2] * item % 16 == 0;
+bool ln_on(const void* p, const int64_t s[3], int item, int bytes) {
+  return host::aligned(p, bytes) && s[0] * item % bytes == 0 && s[1] * item % bytes == 0 &&
+         s[2] * item % bytes == 0;
 }
 LnLayout ln_layout(int B, int H, int S, const int64_t s[3]) {
   const bool heads = H == 1 || s[1] == S * s[2];
@@ -160,8 +163,11 @@ VIDATTN_API int vidattn_layernorm(const void* x, const void* weight, const void*
   p.params_bf16 = param_type == VIDATTN_BF16;
   p.inv_n = 1.f / float(N);
   p.eps = float(eps);
-  const bool vec = N % 8 == 0 && ln_vector(x, x_strides, item) && ln_vector(y, y_strides, item);
-  const LnChoice c = ln_choose(false, x_type == VIDATTN_BF16, vec, N);
+  auto fits = [&](int bytes) {
+    return N * item % bytes == 0 && ln_on(x, x_strides, item, bytes) &&
+           ln_on(y, y_strides, item, bytes);
+  };
+  const LnChoice c = ln_choose(false, x_type == VIDATTN_BF16, fits(16) ? 16 : fits(4) ? 4 : 2, N);
   const int grid = ln_grid(dev, sms, c, p.rows);
   if (grid < 1) return VIDATTN_ERR_CUDA;
   c.kernel<<<grid, c.threads, c.ring, reinterpret_cast<cudaStream_t>(stream_)>>>(p);
@@ -170,7 +176,7 @@ VIDATTN_API int vidattn_layernorm(const void* x, const void* weight, const void*
 
 VIDATTN_API int64_t vidattn_layernorm_bwd_workspace(int B, int H, int S, int N, int x_type) {
   if (!ln_sizes_ok(B, H, S, N) || !ln_type_ok(x_type)) return -1;
-  const LnChoice c = ln_choose(true, x_type == VIDATTN_BF16, true, N);
+  const LnChoice c = ln_choose(true, x_type == VIDATTN_BF16, 16, N);
   return (ln_bwd_parts(c, int64_t(B) * H * S) * 2 * N * 4 + 255) & ~int64_t(255);
 }
 
@@ -228,9 +234,11 @@ VIDATTN_API int vidattn_layernorm_bwd(const void* dy, const void* x, const float
   p.div_h = make_fastdiv(uint32_t(H));
   p.params_bf16 = param_type == VIDATTN_BF16;
   p.inv_n = 1.f / float(N);
-  const bool vec = N % 8 == 0 && ln_vector(x, x_strides, item) && ln_vector(dy, dy_strides, item) &&
-                   ln_vector(dx, dx_strides, item);
-  const LnChoice c = ln_choose(true, x_type == VIDATTN_BF16, vec, N);
+  auto fits = [&](int bytes) {
+    return N * item % bytes == 0 && ln_on(x, x_strides, item, bytes) &&
+           ln_on(dy, dy_strides, item, bytes) && ln_on(dx, dx_strides, item, bytes);
+  };
+  const LnChoice c = ln_choose(true, x_type == VIDATTN_BF16, fits(16) ? 16 : fits(4) ? 4 : 2, N);
   int grid = ln_grid(dev, sms, c, p.rows);
   if (grid < 1) return VIDATTN_ERR_CUDA;
   grid = int(std::min<int64_t>(grid, ln_bwd_parts(c, p.rows)));
