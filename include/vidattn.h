@@ -32,9 +32,8 @@
  * CUDA graphs: once set up, vidattn_fwd, vidattn_fwd_ex, vidattn_fwd_window,
  * vidattn_fwd_noalloc, vidattn_rope3d and vidattn_rope3d_scaled, vidattn_bwd and
  * the layer norm's calls enqueue kernel launches (memsets where there is nothing
- * to compute) on `stream`
- * and nothing else, so they can be captured into a graph.  Set-up happens on
- * the first call on a device (kernel attributes, symbol addresses, occupancy
+ * to compute) on `stream` and nothing else, so they can be captured into a
+ * graph.  Set-up happens on the first call on a device (kernel attributes, symbol addresses, occupancy
  * queries: host calls only) and, for the calls that use scratch (ids or a
  * window), on the first call on a stream or with a larger shape (cudaMalloc
  * after synchronising that stream, which a capture does not allow).  So make
@@ -345,9 +344,11 @@ VIDATTN_API int64_t vidattn_bwd_workspace(int has_ids, int B, int H, int S_q, in
  *   B, H >= 1; S >= 0; 1 <= N <= 16384; B*H*S < 2^31; eps >= 0, finite.
  *
  * Any alignment of the type works; rows on 16-byte boundaries with N a
- * multiple of 8 are the fast ones.  Arithmetic in fp32, the variance about the
- * mean (not as a difference of squares), y rounded once.  One kernel, no
- * allocation, no scratch.  Errors before anything is enqueued: NULL,
+ * multiple of 16 bytes are the fast ones, bf16 rows on odd places or of odd
+ * length the slow ones.  The order of a row's sums goes by its alignment.
+ * Arithmetic in fp32, the variance about the mean (not as a difference of
+ * squares), y rounded once.  One kernel, no allocation, no scratch.  Errors
+ * before anything is enqueued: NULL,
  * MISALIGNED (to the type's size), BAD_SHAPE for the rest.
  */
 VIDATTN_API int vidattn_layernorm(const void* x, const void* weight, const void* bias, void* y,

@@ -251,3 +251,33 @@ def test_differences():
         # fp32 gradients: each element to about 1e-6 of the largest term
         tol = 1e-5 * (grad.double().abs() * u.abs()).sum().item() + 1e-5 * u.abs().sum().item()
         assert abs((grad.double() * u).sum().item() - slope) <= tol
+
+
+@pytest.mark.parametrize("N", [1, 2, 3, 31, 63, 64, 127, 128, 255, 511, 513, 1023, 1024, 2047, 5119])
+@pytest.mark.parametrize("off,pitch", [(0, 0), (1, 0), (1, 1), (3, 2), (2, 4)])
+def test_bf16_rows_on_any_place(N, off, pitch):
+    """Rows that start on any 2 bytes, the same or another in every row, of even
+    and odd length, into rows of other places; nothing beside them is written."""
+    rows = 70
+    w, b = randn(2, N, scale=0.2, shift=1.0), randn(3, N, scale=0.2)
+
+    def place(o, seed=None, fill=None):
+        buf = randn(seed, rows * (N + pitch) + 16, dtype=BF) if seed else \
+            torch.full((rows * (N + pitch) + 16,), fill, dtype=BF, device="cuda")
+        return buf, buf[o:].as_strided((rows, N), (N + pitch, 1), buf.storage_offset() + o)
+
+    x, dy = place(off, 1)[1], place(off + 1, 5)[1]
+    buf, out = place(off + 2, fill=7.0)
+    y, mean, rstd = binding.layer_norm(x, w, b, 1e-3, out=out)
+    check_fwd(x, w, b, 1e-3, y, mean, rstd)
+    dbuf, dout = place(off + 3, fill=7.0)
+    dx, dw, db = binding.layer_norm_bwd(dy, x, mean, rstd, w, out=dout)
+    check_bwd(dy, x, mean, rstd, w, dx, dw, db)
+    for whole, o in ((buf, off + 2), (dbuf, off + 3)):
+        inside = torch.zeros(whole.shape, dtype=torch.bool, device="cuda")
+        inside.as_strided((rows, N), (N + pitch, 1), o).fill_(True)
+        assert bool((whole[~inside] == 7.0).all()), "written beside a row"
+    # in place, from the same places (the order of a row's sums goes by its place)
+    whole, here = place(off, 1)
+    y, mean, rstd = binding.layer_norm(here, w, b, 1e-3, out=here)
+    check_fwd(x, w, b, 1e-3, y, mean, rstd)

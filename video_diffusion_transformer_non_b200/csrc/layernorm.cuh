@@ -17,14 +17,17 @@
 // filled by cp.async up to three turns ahead, each thread copying and reading its
 // own features (so the ring needs no barrier).  Rows on 16-byte boundaries with
 // N a multiple of 16 bytes move in pieces of 16 bytes, the others in pieces of 4;
-// bf16 rows on odd places or of odd length, which cp.async cannot copy, go
-// feature by feature through registers.
+// bf16 rows on odd places or of odd length are put together from 4-byte pieces
+// of neighbouring lanes, with a barrier a turn.
 //
 // Measured (B200): 32760 rows of 5120 bf16 in 125 us (5.4 TB/s, 82 % of the
-// copy rate), backward 218 us (4.6 TB/s); 524160 rows of 128, backward, from a
-// [B,S,H,D] projection 78 us (5.2 TB/s).  Instruction issue bounds it (51 - 64 %
-// of the slots); a deeper ring, one CTA of twice the threads or 32 features a
-// thread were slower.
+// copy rate), backward 193 us (5.2 TB/s); 524160 rows of 128, backward, from a
+// [B,S,H,D] projection 74 us (5.5 TB/s).  16000 rows, forward and backward: of
+// 5118 bf16 (pieces of 4 bytes) 82 and 148 us, of 5119 (odd) 167 and 233, of
+// 5120 fp32 119 and 174, of 5119 fp32 144 and 222; feature by feature through
+// registers the bf16 ones took 258 and 572.  Instruction issue bounds it (51 -
+// 64 % of the slots); a deeper ring, one CTA of twice the threads or 32
+// features a thread were slower.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -99,14 +102,19 @@ __device__ __forceinline__ int ln_col(int e, int lane, int lanes) {
 }
 
 // 8 kC features of one row, as read: X is float or uint16_t (bf16), in pieces
-// of kV (16 or 4 bytes; 2 for bf16 rows on odd places).  N is a multiple of kV.
+// of kV (16 or 4 bytes), of which N is a multiple.  bf16 with kV = 1: rows of
+// any length on any place.  Their lanes hold pairs of features too; what is
+// copied are the 4 aligned bytes that hold two features of the row, which on an
+// odd place are one lane's second and the next one's first, and the one or two
+// features left at the row's ends are read as they are used.
 template <typename X, int kC, int kV>
 struct LnFrag {
+  static constexpr bool kOdd = sizeof(X) == 2 && kV == 1;
+  static constexpr int kCols = kOdd ? 2 : kV;   // neighbouring features of a lane
   static constexpr int kE = 8 * kC;
-  static constexpr int kPieces = kE / kV;
-  static constexpr int kPieceBytes = kV * int(sizeof(X));
-  static constexpr bool kAsync = kPieceBytes >= 4;   // by cp.async
-  static constexpr bool kPacked = sizeof(X) == 2 && kAsync;
+  static constexpr int kPieces = kE / kCols;
+  static constexpr int kPieceBytes = kCols * int(sizeof(X));
+  static constexpr bool kPacked = sizeof(X) == 2;
   static constexpr int kWords = kPacked ? kE / 2 : kE;
   uint32_t r[kWords];
 
@@ -114,21 +122,25 @@ struct LnFrag {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) r[i] = 0u;
   }
+  // 1: the row starts on the second half of 4 aligned bytes
+  static __device__ __forceinline__ int shift(const X* row) {
+    return kOdd ? int(reinterpret_cast<uintptr_t>(row) >> 1) & 1 : 0;
+  }
   // Features at and behind N read as 0.
   __device__ __forceinline__ void load(const X* row, int lane, int lanes, int N) {
     clear();
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int at = (i * lanes + lane) * kV;
+      const int at = (i * lanes + lane) * kCols;
       if (at >= N) continue;
       uint32_t* d = r + i * (kWords / kPieces);
-      if constexpr (kPieceBytes == 16) {
+      if constexpr (kOdd) {
+        d[0] = uint32_t(row[at]) | (at + 1 < N ? uint32_t(row[at + 1]) << 16 : 0u);
+      } else if constexpr (kPieceBytes == 16) {
         const uint4 v = *reinterpret_cast<const uint4*>(row + at);
         d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
-      } else if constexpr (kPieceBytes == 4) {
-        d[0] = *reinterpret_cast<const uint32_t*>(row + at);
       } else {
-        d[0] = uint32_t(row[at]) << 16;
+        d[0] = *reinterpret_cast<const uint32_t*>(row + at);
       }
     }
   }
@@ -136,30 +148,53 @@ struct LnFrag {
   // a shared address of this thread's.
   static __device__ __forceinline__ void copy(uint32_t ring, uint32_t pitch, const X* row,
                                               int lane, int lanes, int N) {
+    const int sh = shift(row);
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int at = (i * lanes + lane) * kV;
-      if (at >= N) continue;
-      if constexpr (kPieceBytes == 16) ln_copy16(ring + i * pitch, row + at);
-      else ln_copy4(ring + i * pitch, row + at);
+      const int at = (i * lanes + lane) * kCols - sh;
+      if constexpr (kOdd) {
+        if (at >= 0 && at + 1 < N) ln_copy4(ring + i * pitch, row + at);
+      } else {
+        if (at >= N) continue;
+        if constexpr (kPieceBytes == 16) ln_copy16(ring + i * pitch, row + at);
+        else ln_copy4(ring + i * pitch, row + at);
+      }
     }
   }
-  __device__ __forceinline__ void read(uint32_t ring, uint32_t pitch, int lane, int lanes, int N) {
+  static __device__ __forceinline__ uint32_t word(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+  }
+  // kOdd: reads what other lanes of the row copied (a barrier lies between)
+  __device__ __forceinline__ void read(uint32_t ring, uint32_t pitch, const X* row, int lane,
+                                       int lanes, int N) {
+    const int sh = shift(row);
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const bool in = (i * lanes + lane) * kV < N;
+      const int at = (i * lanes + lane) * kCols;
       uint32_t* d = r + i * (kWords / kPieces);
-      if constexpr (kPieceBytes == 16) {
+      if constexpr (kOdd) {
+        const uint32_t mine = ring + i * pitch;
+        d[0] = 0u;
+        if (at >= N) continue;
+        if (sh == 0) {
+          d[0] = at + 1 < N ? word(mine) : uint32_t(row[at]);
+        } else {
+          const uint32_t next = lane + 1 < lanes ? mine + 4 : mine - 4 * lane + pitch;
+          d[0] = at > 0 ? word(mine) >> 16 : uint32_t(row[0]);
+          if (at + 2 < N) d[0] |= word(next) << 16;
+          else if (at + 1 < N) d[0] |= uint32_t(row[at + 1]) << 16;
+        }
+      } else if constexpr (kPieceBytes == 16) {
         d[0] = d[1] = d[2] = d[3] = 0u;
-        if (in)
+        if (at < N)
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
                        : "r"(ring + i * pitch)
                        : "memory");
       } else {
-        d[0] = 0u;
-        if (in)
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(d[0]) : "r"(ring + i * pitch) : "memory");
+        d[0] = at < N ? word(ring + i * pitch) : 0u;
       }
     }
   }
@@ -176,36 +211,42 @@ __device__ __forceinline__ float2 ln_both(float v) { return make_float2(v, v); }
 template <typename X, int kC, int kV>
 __device__ __forceinline__ void ln_store(X* row, int lane, int lanes, int N,
                                          const float2 (&v)[4 * kC]) {
+  using Frag = LnFrag<X, kC, kV>;
+  const int sh = Frag::shift(row);
 #pragma unroll
-  for (int i = 0; i < 8 * kC / kV; ++i) {
-    const int at = (i * lanes + lane) * kV;
+  for (int i = 0; i < Frag::kPieces; ++i) {
+    const int at = (i * lanes + lane) * Frag::kCols;
     if (at >= N) continue;
-    if constexpr (kV >= 2) {
-      const float2* s = v + i * (kV / 2);
-      if constexpr (sizeof(X) == 4)
+    const float2* s = v + i * Frag::kCols / 2;
+    if constexpr (sizeof(X) == 4) {
+      if constexpr (kV == 4)
         *reinterpret_cast<float4*>(row + at) = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
-      else if constexpr (kV == 8)
-        *reinterpret_cast<uint4*>(row + at) =
-            make_uint4(pack_bf16x2(s[0].x, s[0].y), pack_bf16x2(s[1].x, s[1].y),
-                       pack_bf16x2(s[2].x, s[2].y), pack_bf16x2(s[3].x, s[3].y));
       else
-        *reinterpret_cast<uint32_t*>(row + at) = pack_bf16x2(s[0].x, s[0].y);
+        row[at] = (i & 1) ? s[0].y : s[0].x;
+    } else if constexpr (kV == 8) {
+      *reinterpret_cast<uint4*>(row + at) =
+          make_uint4(pack_bf16x2(s[0].x, s[0].y), pack_bf16x2(s[1].x, s[1].y),
+                     pack_bf16x2(s[2].x, s[2].y), pack_bf16x2(s[3].x, s[3].y));
     } else {
-      const float t = (i & 1) ? v[i / 2].y : v[i / 2].x;
-      if constexpr (sizeof(X) == 2) row[at] = ln_to_bf16(t);
-      else row[at] = t;
+      const uint32_t w = pack_bf16x2(s[0].x, s[0].y);
+      if (!Frag::kOdd || (sh == 0 && at + 1 < N)) {
+        *reinterpret_cast<uint32_t*>(row + at) = w;
+      } else {
+        row[at] = uint16_t(w & 0xffffu);
+        if (at + 1 < N) row[at + 1] = uint16_t(w >> 16);
+      }
     }
   }
 }
 
 // This thread's features of weight or bias (null: `none`).
-template <typename P, int kC, int kV>
+template <typename P, int kC, int kCols>
 __device__ __forceinline__ void ln_params_of(const P* src, int lane, int lanes, int N,
                                              float2 (&v)[4 * kC]) {
   P t[8 * kC];
 #pragma unroll
   for (int e = 0; e < 8 * kC; ++e) {
-    const int at = ln_col<kV>(e, lane, lanes);
+    const int at = ln_col<kCols>(e, lane, lanes);
     t[e] = at < N ? __ldg(src + at) : P(0);
   }
 #pragma unroll
@@ -214,16 +255,16 @@ __device__ __forceinline__ void ln_params_of(const P* src, int lane, int lanes, 
     else v[e] = make_float2(t[2 * e], t[2 * e + 1]);
   }
 }
-template <int kC, int kV>
+template <int kC, int kCols>
 __device__ __forceinline__ void ln_params(const void* src, int bf16, int lane, int lanes, int N,
                                           float none, float2 (&v)[4 * kC]) {
   if (src == nullptr) {
 #pragma unroll
     for (int e = 0; e < 4 * kC; ++e) v[e] = ln_both(none);
   } else if (bf16) {
-    ln_params_of<uint16_t, kC, kV>(static_cast<const uint16_t*>(src), lane, lanes, N, v);
+    ln_params_of<uint16_t, kC, kCols>(static_cast<const uint16_t*>(src), lane, lanes, N, v);
   } else {
-    ln_params_of<float, kC, kV>(static_cast<const float*>(src), lane, lanes, N, v);
+    ln_params_of<float, kC, kCols>(static_cast<const float*>(src), lane, lanes, N, v);
   }
   // kept in registers, not read again for every row
 #pragma unroll
@@ -269,7 +310,7 @@ template <typename X, int kLanes, int kC, int kR, int kV, int kMaxThreads, int k
 struct LnWalk {
   static constexpr bool kBlock = kLanes == 0;
   using Frag = LnFrag<X, kC, kV>;
-  static constexpr int kS = Frag::kAsync ? ln_stages(kMaxThreads, kR, kTensors, Frag::kWords * 4) : 0;
+  static constexpr int kS = ln_stages(kMaxThreads, kR, kTensors, Frag::kWords * 4);
   static constexpr bool kRing = kS >= 2;
   int lanes, lane, groups, group;
   uint32_t row, step, pitch, stage, ring, in, out;   // in, out: ring addresses of this thread's
@@ -337,15 +378,20 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_fwd_kernel(const LnPara
     fetch(t.row);
   }
   float2 w[kE / 2], b[kE / 2];
-  ln_params<kC, kV>(p.w, p.params_bf16, lane, lanes, p.N, 1.f, w);
-  ln_params<kC, kV>(p.b, p.params_bf16, lane, lanes, p.N, 0.f, b);
+  ln_params<kC, Frag::kCols>(p.w, p.params_bf16, lane, lanes, p.N, 1.f, w);
+  ln_params<kC, Frag::kCols>(p.b, p.params_bf16, lane, lanes, p.N, 0.f, b);
   for (int turn = 0; t.any(p); turn ^= 1, t.row += t.step) {
     Frag cur[kR];
     if constexpr (kRing) {
       fetch(t.row + (kS - 1) * t.step);
       ln_wait<kRing ? kS - 1 : 0>();
+      if (Frag::kOdd) kBlock ? __syncthreads() : __syncwarp();
 #pragma unroll
-      for (int i = 0; i < kR; ++i) cur[i].read(t.slot(t.out, i, 0), t.pitch, lane, lanes, p.N);
+      for (int i = 0; i < kR; ++i) {
+        const uint32_t row = min(t.row + i * t.groups, uint32_t(p.rows - 1));
+        cur[i].read(t.slot(t.out, i, 0), t.pitch,
+                    Frag::kOdd ? x + ln_offset(p, p.lx, row) : nullptr, lane, lanes, p.N);
+      }
       t.next(t.out);
     } else {
 #pragma unroll
@@ -373,10 +419,10 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_fwd_kernel(const LnPara
       for (int e = 0; e < kE / 2; ++e) {
         d[i][e] = fadd2(d[i][e], ln_both(-mean[i]));
         if (kV >= 2) {   // features behind N add nothing
-          if (ln_col<kV>(2 * e, lane, lanes) < p.N) s = ffma2(d[i][e], d[i][e], s);
+          if (ln_col<Frag::kCols>(2 * e, lane, lanes) < p.N) s = ffma2(d[i][e], d[i][e], s);
         } else {
-          if (ln_col<kV>(2 * e, lane, lanes) < p.N) s.x = fmaf(d[i][e].x, d[i][e].x, s.x);
-          if (ln_col<kV>(2 * e + 1, lane, lanes) < p.N) s.y = fmaf(d[i][e].y, d[i][e].y, s.y);
+          if (ln_col<Frag::kCols>(2 * e, lane, lanes) < p.N) s.x = fmaf(d[i][e].x, d[i][e].x, s.x);
+          if (ln_col<Frag::kCols>(2 * e + 1, lane, lanes) < p.N) s.y = fmaf(d[i][e].y, d[i][e].y, s.y);
         }
       }
       var[i] = s.x + s.y;
@@ -479,7 +525,7 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_bwd_kernel(const LnPara
   } else {
     fetch(t.row);
   }
-  ln_params<kC, kV>(p.w, p.params_bf16, lane, lanes, p.N, 1.f, w);
+  ln_params<kC, Frag::kCols>(p.w, p.params_bf16, lane, lanes, p.N, 1.f, w);
   for (int turn = 0; t.any(p); turn ^= 1, t.row += t.step) {
     Frag cx[kR], cg[kR];
     float m[kR], r[kR], c[2 * kR];
@@ -491,13 +537,17 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_bwd_kernel(const LnPara
     if constexpr (kRing) {
       fetch(t.row + (kS - 1) * t.step);
       ln_wait<kRing ? kS - 1 : 0>();
-      __syncwarp();   // the statistics came by two of the lanes
+      if (Frag::kOdd && kBlock) __syncthreads();
+      else __syncwarp();   // the statistics came by two of the lanes
 #pragma unroll
       for (int i = 0; i < kR; ++i) {
         const float2 st = stats[st_out][i][owner];
         m[i] = -st.x, r[i] = st.y;
-        cx[i].read(t.slot(t.out, i, 0), t.pitch, lane, lanes, p.N);
-        cg[i].read(t.slot(t.out, i, 1), t.pitch, lane, lanes, p.N);
+        const uint32_t row = min(t.row + i * t.groups, uint32_t(p.rows - 1));
+        cx[i].read(t.slot(t.out, i, 0), t.pitch,
+                   Frag::kOdd ? x + ln_offset(p, p.lx, row) : nullptr, lane, lanes, p.N);
+        cg[i].read(t.slot(t.out, i, 1), t.pitch,
+                   Frag::kOdd ? dy + ln_offset(p, p.ldy, row) : nullptr, lane, lanes, p.N);
         if (t.row + i * t.groups >= p.rows) {   // no row: no share
           cx[i].clear(), cg[i].clear();
           m[i] = r[i] = 0.f;
@@ -555,7 +605,7 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_bwd_kernel(const LnPara
   if constexpr (kBlock) {
 #pragma unroll
     for (int e = 0; e < kE; ++e) {
-      const int at = ln_col<kV>(e, lane, lanes);
+      const int at = ln_col<Frag::kCols>(e, lane, lanes);
       if (at < p.N) {
         part[at] = value(dw, e);
         part[p.N + at] = value(db, e);
@@ -577,7 +627,7 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_bwd_kernel(const LnPara
         float t = 0.f;
 #pragma unroll
         for (int k = 0; k < kLnThreads / 32; ++k) t += sums[k][i];
-        const int at = ln_col<kV>(i / kLanes, i % kLanes, kLanes);
+        const int at = ln_col<Frag::kCols>(i / kLanes, i % kLanes, kLanes);
         if (at < p.N) part[which * p.N + at] = t;
       }
       __syncthreads();

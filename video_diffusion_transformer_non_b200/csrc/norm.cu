@@ -35,7 +35,7 @@ template <typename X, int kLanes, int kC, int kR, int kV, int kMaxThreads, int k
 LnChoice ln_form(bool bwd, int threads) {
   using Frag = LnFrag<X, kC, kV>;
   const int piece = Frag::kWords * 4, tensors = bwd ? 2 : 1;
-  const int stages = Frag::kAsync ? ln_stages(kMaxThreads, kR, tensors, piece) : 0;
+  const int stages = ln_stages(kMaxThreads, kR, tensors, piece);
   return LnChoice{bwd ? ln_bwd_kernel<X, kLanes, kC, kR, kV, kMaxThreads, kBwd>
                       : ln_fwd_kernel<X, kLanes, kC, kR, kV, kMaxThreads, kFwd>,
                   threads, kLanes ? threads / kLanes * kR : kR,
