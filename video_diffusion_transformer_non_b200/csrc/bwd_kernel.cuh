@@ -279,19 +279,24 @@ __device__ __forceinline__ bool bwd_pair_masked(const BwdParams& p, int b, int i
 }
 
 // Which of the 32 columns [x0, x0 + 32) of a score tile row are visible, as
-// bits: lo <= column < hi, and the column's id equal to the row's.
+// bits: lo <= column < hi, and the column's id equal to the row's.  Called by
+// all lanes of a warp, whose rows differ and whose columns are the same: each
+// lane reads one column's id, and every id among them (a few: runs) is compared
+// with all of them by one ballot.
 static __device__ __noinline__ uint32_t bwd_mask32(int x0, int lo, int hi, const int32_t* ids,
                                                   int n_ids, int my_id) {
   uint32_t m = 0;
   const int a = max(lo - x0, 0), e = min(hi - x0, 32);
   if (a < e) m = (~0u >> (32 - (e - a))) << a;
-  if (ids != nullptr && m != 0u) {
-    uint32_t eq = 0;
-#pragma unroll 8
-    for (int x = 0; x < 32; ++x) {
-      const int col = x0 + x;
-      const int id = col < n_ids ? __ldg(ids + col) : 0;
-      if (id == my_id) eq |= 1u << x;
+  if (ids != nullptr) {
+    const int col = x0 + int(threadIdx.x & 31);
+    const int id = col < n_ids ? __ldg(ids + col) : 0;
+    uint32_t eq = 0, left = ~0u;
+    while (left != 0u) {
+      const int one = __shfl_sync(0xffffffffu, id, __ffs(left) - 1);
+      const uint32_t same = __ballot_sync(0xffffffffu, id == one);
+      if (one == my_id) eq = same;
+      left &= ~same;
     }
     m &= eq;
   }
