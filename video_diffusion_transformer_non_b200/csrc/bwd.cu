@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <map>
@@ -27,23 +28,41 @@ int bwd_smem(int D) { return D == 128 ? BwdCfg<128>::kSmemBytes : BwdCfg<64>::kS
 
 int tiles(int S) { return (S + 127) / 128; }
 
+// Tile pairs that the causal limit leaves (all without it), in whole tiles.
+int64_t bwd_pairs(int n_q, int n_kv, bool causal, int off) {
+  if (!causal) return int64_t(n_q) * n_kv;
+  // query tile i sees i + first key tiles, between none and all
+  const int64_t first = (int64_t(off) + 127 >= 0 ? (off + 127) / 128 : -((-int64_t(off)) / 128)) + 1;
+  const int64_t lo = std::min<int64_t>(std::max<int64_t>(1 - first, 0), n_q);
+  const int64_t hi = std::min<int64_t>(std::max<int64_t>(n_kv - first, lo), n_q);
+  return (hi - lo) * first + (hi * (hi - 1) - lo * (lo - 1)) / 2 + (n_q - hi) * n_kv;
+}
+
 // How many ranges a unit's visited tiles are split into.  A unit of `len`
-// tiles costs `cost` products each; with few units the longest one bounds the
-// launch, so it is cut to half of an SM's even share of all work, but not
-// below kBwdMinTiles tiles (the partial sums then cost more than they gain).
-constexpr int kBwdMinTiles = 8;
-int bwd_split(int len, int cost, int64_t total, int requested) {
+// tiles costs `cost` products each, `share` is an SM's part of all products.
+// With few units the longest bounds the launch; but each range has a start, a
+// drain and fp32 sums of its own and the adding kernel follows, so a split has
+// to shorten the longest unit by 15 products and by 0.7 shares.  Measured (H,
+// S_q x S_kv, D = 128, us): 2, 4096^2, a unit of 1.3 shares: 60 whole, 66 in 2;
+// 4, 1323^2, 1.9 shares but 11 tiles: 29 and 35; 4, 2398^2 causal, 2.1 shares:
+// 41 and 47; 1, 4096^2, 2.7 shares: 58 whole, 43 in 2, 48 in 3; 1, 8192^2
+// causal, 2.6 shares: 104 whole, 70 in 2; 1, 2048^2, 5.3 shares: 35 whole, 30
+// in 2, 25 in 4, 29 in 6.
+constexpr int kBwdMinTiles = 4;
+int bwd_split(int len, int cost, int64_t share, int requested) {
   if (requested > 0) return requested;
-  const int64_t share = total / (2 * 148);
-  const int64_t floor_cost = int64_t(kBwdMinTiles) * cost;
-  const int64_t most = share > floor_cost ? share : floor_cost;
-  int64_t n = (int64_t(len) * cost + most - 1) / most;
-  if (n > kBwdMaxSplit) n = kBwdMaxSplit;
-  return n < 1 ? 1 : int(n);
+  const int64_t unit = int64_t(len) * cost;
+  share = std::max<int64_t>(share, 1);
+  if (10 * unit <= 16 * share) return 1;
+  int64_t n = (20 * unit + 13 * share) / (26 * share);   // unit / (1.3 share), to the nearest
+  n = std::min({std::max<int64_t>(n, 2), int64_t(kBwdMaxSplit),
+                std::max<int64_t>(len / kBwdMinTiles, 1)});
+  return unit - unit / n < 15 + 7 * share / 10 ? 1 : int(n);
 }
 
 struct BwdPlan {
   int n_q, n_kv, kv_split, q_split;
+  bool kv_first;   // the kind with the longer units goes first
   size_t stats, sums, part_kv, part_q, bytes;   // offsets, and the whole size
 };
 
@@ -53,9 +72,11 @@ BwdPlan bwd_plan(bool ids, int B, int H, int S_q, int S_kv, int D, int flags) {
   r.n_q = tiles(S_q);
   r.n_kv = tiles(S_kv);
   const int requested = (flags >> 8) & 0xFF;
-  const int64_t total = BH * r.n_q * r.n_kv * 7;
-  r.kv_split = bwd_split(r.n_q, 4, total, requested);
-  r.q_split = bwd_split(r.n_kv, 3, total, requested);
+  const bool causal = (flags & VIDATTN_CAUSAL) != 0;
+  const int64_t share = BH * bwd_pairs(r.n_q, r.n_kv, causal, S_kv - S_q) * 7 / 148;
+  r.kv_split = bwd_split(r.n_q, 4, share, requested);
+  r.q_split = bwd_split(r.n_kv, 3, share, requested);
+  r.kv_first = int64_t(r.n_q) * 4 * r.q_split >= int64_t(r.n_kv) * 3 * r.kv_split;
   auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
   size_t at = 0;
   r.stats = at;
@@ -198,6 +219,8 @@ VIDATTN_API int vidattn_bwd(const void* q, const void* k, const void* v, const v
   p.n_kv_split = plan.kv_split;
   p.n_q_split = plan.q_split;
   p.n_kv_units = int(kv_units);
+  p.n_q_units = int(n_units - kv_units);
+  p.kv_first = plan.kv_first;
   p.causal = (flags & VIDATTN_CAUSAL) ? 1 : 0;
   p.causal_off = S_kv - S_q;
   p.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);

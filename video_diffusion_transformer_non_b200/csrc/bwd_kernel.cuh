@@ -60,7 +60,8 @@ struct BwdParams {
   int BH, H, S_q, S_kv;
   int n_q_tiles, n_kv_tiles;
   int n_kv_split, n_q_split;
-  int n_kv_units;           // B*H*n_kv_tiles*n_kv_split, launched first
+  int n_kv_units, n_q_units;   // B*H*tiles*split of each kind
+  int kv_first;
   int causal, causal_off;
   float c;                  // scale * log2(e)
   float scale;
@@ -751,10 +752,10 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
   }
 }
 
-// One CTA per unit: the KV units (four products a tile pair, the longer ones)
-// first, each kind with the split fastest, then the tile, then (b, h): the
-// units of one head run close together and share its tiles in L2.  With the
-// causal limit the longest tiles of a head go first.
+// One CTA per unit: the kind with the longer units first, each kind with the
+// split fastest, then the tile, then (b, h): the units of one head run close
+// together and share its tiles in L2.  With the causal limit the longest tiles
+// of a head go first.
 template <int D>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     vidattn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -796,13 +797,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
 
   int u = blockIdx.x;
-  if (u < p.n_kv_units) {
+  const int n_first = p.kv_first ? p.n_kv_units : p.n_q_units;
+  const bool kv = (u < n_first) == (p.kv_first != 0);
+  if (u >= n_first) u -= n_first;
+  if (kv) {
     const int split = u % p.n_kv_split;
     u /= p.n_kv_split;
     bwd_unit<D, true>(tm_q, tm_k, tm_v, tm_do, p, sbase, smem, u / p.n_kv_tiles,
                             u % p.n_kv_tiles, split, p.n_kv_split);
   } else {
-    u -= p.n_kv_units;
     const int split = u % p.n_q_split;
     u /= p.n_q_split;
     const int t = u % p.n_q_tiles;
