@@ -104,6 +104,14 @@ def test_row_counts(rows, N):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N", [1024, 5120, 5121, 6143, 6144, 8184])
+def test_wide_rows_over_several_turns(N, dtype):
+    """An odd number of rows, more than two turns of every CTA."""
+    x = randn(N, 1501, N, dtype=dtype, scale=1.5, shift=0.3)
+    both(x, randn(N + 1, N, scale=0.2, shift=1.0), randn(N + 2, N, scale=0.2))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("B,H,S,N", [(2, 5, 77, 128), (1, 3, 200, 64), (3, 2, 50, 100),
                                      (2, 2, 9, 2000), (1, 1, 6, 1536)])
 def test_strided_rows(dtype, B, H, S, N):

@@ -20,11 +20,11 @@
 // bf16 rows on odd places or of odd length are put together from 4-byte pieces
 // of neighbouring lanes, with a barrier a turn.
 //
-// Measured (B200): 32760 rows of 5120 bf16 in 125 us (5.4 TB/s, 82 % of the
+// Measured (B200): 32760 rows of 5120 bf16 in 112 us (6.0 TB/s, 91 % of the
 // copy rate), backward 193 us (5.2 TB/s); 524160 rows of 128, backward, from a
 // [B,S,H,D] projection 74 us (5.5 TB/s).  16000 rows, forward and backward: of
-// 5118 bf16 (pieces of 4 bytes) 82 and 148 us, of 5119 (odd) 167 and 233, of
-// 5120 fp32 119 and 174, of 5119 fp32 144 and 222; feature by feature through
+// 5118 bf16 (pieces of 4 bytes) 88 and 152 us, of 5119 (odd) 135 and 237, of
+// 5120 fp32 116 and 178, of 5119 fp32 147 and 227; feature by feature through
 // registers the bf16 ones took 258 and 572.  Instruction issue bounds it (51 -
 // 64 % of the slots); a deeper ring, one CTA of twice the threads or 32
 // features a thread were slower.

@@ -28,39 +28,50 @@ struct LnChoice {
   int ring, ring_max;  // bytes of shared memory, and with the most threads
 };
 
-// kLanes of a warp a row (0: the CTA), kC chunks of 8 features a thread, kR
-// rows a thread at a time; registers for kFwd (kBwd) CTAs on an SM: the reductions
-// leave a CTA idle, the next one fills in.
-template <typename X, int kLanes, int kC, int kR, int kV, int kMaxThreads, int kFwd, int kBwd>
+// kLanes of a warp a row (0: the CTA), kC chunks of 8 features a thread; forward
+// (backward) kRf (kRb) rows a thread at a time and registers for kFwd (kBwd) CTAs
+// on an SM: the reductions leave a CTA idle, its other row or the next CTA fills
+// in.  The backward pass has no registers for a second long row.
+template <typename X, int kLanes, int kC, int kRf, int kRb, int kV, int kMaxThreads, int kFwd,
+          int kBwd>
 LnChoice ln_form(bool bwd, int threads) {
   using Frag = LnFrag<X, kC, kV>;
-  const int piece = Frag::kWords * 4, tensors = bwd ? 2 : 1;
-  const int stages = ln_stages(kMaxThreads, kR, tensors, piece);
-  return LnChoice{bwd ? ln_bwd_kernel<X, kLanes, kC, kR, kV, kMaxThreads, kBwd>
-                      : ln_fwd_kernel<X, kLanes, kC, kR, kV, kMaxThreads, kFwd>,
-                  threads, kLanes ? threads / kLanes * kR : kR,
-                  stages >= 2 ? stages * threads * kR * tensors * piece : 0,
-                  stages >= 2 ? stages * kMaxThreads * kR * tensors * piece : 0};
+  const int piece = Frag::kWords * 4, tensors = bwd ? 2 : 1, rows = bwd ? kRb : kRf;
+  const int stages = ln_stages(kMaxThreads, rows, tensors, piece);
+  return LnChoice{bwd ? ln_bwd_kernel<X, kLanes, kC, kRb, kV, kMaxThreads, kBwd>
+                      : ln_fwd_kernel<X, kLanes, kC, kRf, kV, kMaxThreads, kFwd>,
+                  threads, kLanes ? threads / kLanes * rows : rows,
+                  stages >= 2 ? stages * threads * rows * tensors * piece : 0,
+                  stages >= 2 ? stages * kMaxThreads * rows * tensors * piece : 0};
 }
 
-// The smallest form that holds a row of N features in registers.
+// The smallest form that holds a row of N features in registers.  Forward, one
+// and two rows at a time (bf16, us): 32760 x 5120 129 and 114, 16000 x 5119 172
+// and 136, 32760 x 2560 63.5 and 65.6, 16000 x 8192 123 and 112, 100000 x 768 78
+// and 63; 200000 x 384 62.4 and 63.5, so one there.  32760 x 6144 172 with one CTA
+// on an SM, 141 with two.  Fewer rows than the device has warps of this form: one a
+// warp (226 x 1001 fp32: 8.2, 10.2 with two).
 template <typename X, int kV>
-LnChoice ln_choose_x(bool bwd, int N) {
-  if (N <= 64) return ln_form<X, 8, 1, 2, kV, kLnThreads, 3, 2>(bwd, kLnThreads);
-  if (N <= 128) return ln_form<X, 16, 1, 2, kV, kLnThreads, 3, 2>(bwd, kLnThreads);
-  if (N <= 256) return ln_form<X, 32, 1, 2, kV, kLnThreads, 3, 2>(bwd, kLnThreads);
-  if (N <= 512) return ln_form<X, 32, 2, 1, kV, kLnThreads, 2, 2>(bwd, kLnThreads);
-  if (N <= 1024) return ln_form<X, 32, 4, 1, kV, kLnThreads, 1, 1>(bwd, kLnThreads);
+LnChoice ln_choose_x(bool bwd, int N, int64_t rows) {
+  if (N <= 64) return ln_form<X, 8, 1, 2, 2, kV, kLnThreads, 3, 2>(bwd, kLnThreads);
+  if (N <= 128) return ln_form<X, 16, 1, 2, 2, kV, kLnThreads, 3, 2>(bwd, kLnThreads);
+  if (N <= 256) return ln_form<X, 32, 1, 2, 2, kV, kLnThreads, 3, 2>(bwd, kLnThreads);
+  if (N <= 512) return ln_form<X, 32, 2, 1, 1, kV, kLnThreads, 2, 2>(bwd, kLnThreads);
+  if (N <= 1024 && rows <= 148 * 8)
+    return ln_form<X, 32, 4, 1, 1, kV, kLnThreads, 1, 1>(bwd, kLnThreads);
+  if (N <= 1024) return ln_form<X, 32, 4, 2, 1, kV, kLnThreads, 1, 1>(bwd, kLnThreads);
   const int threads = (N + 511) / 512 * 32;
-  if (threads <= 320) return ln_form<X, 0, 2, 1, kV, 320, 2, 2>(bwd, threads);
-  if (threads <= 512) return ln_form<X, 0, 2, 1, kV, 512, 1, 1>(bwd, threads);
-  return ln_form<X, 0, 2, 1, kV, 1024, 1, 1>(bwd, threads);
+  if (threads <= 320) return ln_form<X, 0, 2, 2, 1, kV, 320, 2, 2>(bwd, threads);
+  if (threads <= 384) return ln_form<X, 0, 2, 2, 1, kV, 384, 2, 1>(bwd, threads);
+  if (threads <= 512) return ln_form<X, 0, 2, 2, 1, kV, 512, 1, 1>(bwd, threads);
+  return ln_form<X, 0, 2, 1, 1, kV, 1024, 1, 1>(bwd, threads);
 }
 // piece: 16, 4 or 2, the bytes that every row's start and length are a multiple of.
-LnChoice ln_choose(bool bwd, bool bf16, int piece, int N) {
-  if (!bf16) return piece == 16 ? ln_choose_x<float, 4>(bwd, N) : ln_choose_x<float, 1>(bwd, N);
-  if (piece == 16) return ln_choose_x<uint16_t, 8>(bwd, N);
-  return piece == 4 ? ln_choose_x<uint16_t, 2>(bwd, N) : ln_choose_x<uint16_t, 1>(bwd, N);
+LnChoice ln_choose(bool bwd, bool bf16, int piece, int N, int64_t rows) {
+  if (!bf16)
+    return piece == 16 ? ln_choose_x<float, 4>(bwd, N, rows) : ln_choose_x<float, 1>(bwd, N, rows);
+  if (piece == 16) return ln_choose_x<uint16_t, 8>(bwd, N, rows);
+  return piece == 4 ? ln_choose_x<uint16_t, 2>(bwd, N, rows) : ln_choose_x<uint16_t, 1>(bwd, N, rows);
 }
 
 // CTAs of a launch: enough for all rows, at most what the device holds at once
@@ -167,7 +178,8 @@ VIDATTN_API int vidattn_layernorm(const void* x, const void* weight, const void*
     return N * item % bytes == 0 && ln_on(x, x_strides, item, bytes) &&
            ln_on(y, y_strides, item, bytes);
   };
-  const LnChoice c = ln_choose(false, x_type == VIDATTN_BF16, fits(16) ? 16 : fits(4) ? 4 : 2, N);
+  const LnChoice c = ln_choose(false, x_type == VIDATTN_BF16, fits(16) ? 16 : fits(4) ? 4 : 2, N,
+                               p.rows);
   const int grid = ln_grid(dev, sms, c, p.rows);
   if (grid < 1) return VIDATTN_ERR_CUDA;
   c.kernel<<<grid, c.threads, c.ring, reinterpret_cast<cudaStream_t>(stream_)>>>(p);
@@ -176,8 +188,9 @@ VIDATTN_API int vidattn_layernorm(const void* x, const void* weight, const void*
 
 VIDATTN_API int64_t vidattn_layernorm_bwd_workspace(int B, int H, int S, int N, int x_type) {
   if (!ln_sizes_ok(B, H, S, N) || !ln_type_ok(x_type)) return -1;
-  const LnChoice c = ln_choose(true, x_type == VIDATTN_BF16, 16, N);
-  return (ln_bwd_parts(c, int64_t(B) * H * S) * 2 * N * 4 + 255) & ~int64_t(255);
+  const int64_t rows = int64_t(B) * H * S;
+  const LnChoice c = ln_choose(true, x_type == VIDATTN_BF16, 16, N, rows);
+  return (ln_bwd_parts(c, rows) * 2 * N * 4 + 255) & ~int64_t(255);
 }
 
 VIDATTN_API int vidattn_layernorm_bwd(const void* dy, const void* x, const float* mean,
@@ -238,7 +251,8 @@ VIDATTN_API int vidattn_layernorm_bwd(const void* dy, const void* x, const float
     return N * item % bytes == 0 && ln_on(x, x_strides, item, bytes) &&
            ln_on(dy, dy_strides, item, bytes) && ln_on(dx, dx_strides, item, bytes);
   };
-  const LnChoice c = ln_choose(true, x_type == VIDATTN_BF16, fits(16) ? 16 : fits(4) ? 4 : 2, N);
+  const LnChoice c = ln_choose(true, x_type == VIDATTN_BF16, fits(16) ? 16 : fits(4) ? 4 : 2, N,
+                               p.rows);
   int grid = ln_grid(dev, sms, c, p.rows);
   if (grid < 1) return VIDATTN_ERR_CUDA;
   grid = int(std::min<int64_t>(grid, ln_bwd_parts(c, p.rows)));
