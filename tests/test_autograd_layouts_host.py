@@ -1,0 +1,65 @@
+"""The differentiable functions' handling of what autograd hands them: the
+kernels' calls are replaced by their formulas behind the binding's own layout
+checks, so this runs without a GPU."""
+import pytest
+import torch
+
+from video_diffusion_transformer_non_b200 import autograd, binding
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture
+def plain(monkeypatch):
+    def layer_norm(x, weight=None, bias=None, eps=1e-6):
+        binding._rows("x", x)
+        m = x.float().mean(-1)
+        r = ((x.float() - m[..., None]).square().mean(-1) + eps).rsqrt()
+        y = (x.float() - m[..., None]) * r[..., None]
+        if weight is not None:
+            y = y * weight.float() + (0.0 if bias is None else bias.float())
+        return y.to(x.dtype), m, r
+
+    def layer_norm_bwd(dy, x, mean, rstd, weight=None, params=True):
+        binding._rows("dy", dy, x.shape)
+        xh, g = (x.float() - mean[..., None]) * rstd[..., None], dy.float()
+        gw = g if weight is None else g * weight.float()
+        dx = (gw - gw.mean(-1, keepdim=True) - xh * (gw * xh).mean(-1, keepdim=True)) * \
+            rstd[..., None]
+        axes = tuple(range(x.dim() - 1))
+        if weight is None or not params:
+            return dx.to(x.dtype), None, None
+        return dx.to(x.dtype), (g * xh).sum(axes).to(weight.dtype), g.sum(axes).to(weight.dtype)
+
+    monkeypatch.setattr(binding, "layer_norm", layer_norm)
+    monkeypatch.setattr(binding, "layer_norm_bwd", layer_norm_bwd)
+
+
+def losses(N):
+    """Losses whose gradient reaches the norm with a last dim that is not contiguous."""
+    gen = torch.Generator().manual_seed(3)
+    a, c = torch.randn(5, generator=gen), torch.randn(4, N, 3, generator=gen)
+    return dict(sum=lambda y: y.sum(),
+                mean=lambda y: y.mean(),
+                matmul=lambda y: (y.transpose(-1, -2) @ a.to(y).reshape(1, 5, 1)).square().sum(),
+                conv1d=lambda y: torch.nn.functional.conv1d(y.transpose(-1, -2), c.to(y))
+                .square().sum(),
+                column=lambda y: y[..., 1].square().sum())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("loss", ["sum", "mean", "matmul", "conv1d", "column"])
+def test_layer_norm_takes_any_gradient_layout(plain, loss, dtype):
+    """The bits of the call with the same gradient, made contiguous."""
+    N = 6
+    gen = torch.Generator().manual_seed(1)
+    x, w, b = (torch.randn(s, generator=gen).to(dtype).requires_grad_() for s in
+               ((2, 5, N), (N,), (N,)))
+    y = autograd.layer_norm(x, w, b)
+    losses(N)[loss](y).backward()
+    at = y.detach().requires_grad_()
+    dy, = torch.autograd.grad(losses(N)[loss](at), at)
+    _, mean, rstd = binding.layer_norm(x.detach(), w.detach(), b.detach())
+    want = binding.layer_norm_bwd(dy.contiguous(), x.detach(), mean, rstd, w.detach())
+    for t, g in zip((x, w, b), want):
+        assert torch.equal(t.grad, g)

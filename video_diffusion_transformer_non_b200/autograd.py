@@ -74,6 +74,8 @@ class _LayerNorm(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         x, mean, rstd, weight = ctx.saved_tensors
+        if dy.stride(-1) != 1:   # of a plain sum, or of a transposed use
+            dy = dy.contiguous()
         dx, dw, db = binding.layer_norm_bwd(dy, x, mean, rstd, weight,
                                             params=any(ctx.needs_input_grad[1:3]))
         return dx, dw, db if ctx.needs_input_grad[2] else None, None
