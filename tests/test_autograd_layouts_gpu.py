@@ -40,3 +40,18 @@ def test_layer_norm_takes_any_gradient_layout(loss, dtype):
     x.grad = None
     f(autograd.layer_norm(x, w, b), a, c).backward()
     assert torch.isfinite(x.grad).all()
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_rope_of_one_tensor(interleaved):
+    turn = dict(grid=(2, 4, 5), bands=(8, 16, 24), amplitude=1.1, interleaved=interleaved)
+    q, dq = randn(1, 2, 3, 50, 64).requires_grad_(), randn(2, 2, 3, 50, 64)
+    got, none = autograd.rope3d(q, None, **turn)
+    assert none is None
+    got.backward(dq)
+    args = autograd.rope_arguments(turn)
+    assert torch.equal(got, binding.rope3d_scaled(q.detach(), **args)[0])
+    assert torch.equal(q.grad, binding.rope3d_scaled_bwd(dq, **args)[0])
+    q.grad = None
+    autograd.rope3d(q, **turn)[0].sum().backward()   # the gradient comes expanded
+    assert torch.equal(q.grad, binding.rope3d_scaled_bwd(torch.ones_like(dq), **args)[0])

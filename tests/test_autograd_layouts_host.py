@@ -63,3 +63,20 @@ def test_layer_norm_takes_any_gradient_layout(plain, loss, dtype):
     want = binding.layer_norm_bwd(dy.contiguous(), x.detach(), mean, rstd, w.detach())
     for t, g in zip((x, w, b), want):
         assert torch.equal(t.grad, g)
+
+
+def test_rope_of_one_tensor(monkeypatch):
+    """rope3d(q, None) has a gradient as binding.rope3d_scaled(q) has a value."""
+    def turn(q, k=None, sign=1.0, **turn):
+        return 2.0 * sign * q, None if k is None else 2.0 * sign * k
+
+    monkeypatch.setattr(binding, "rope3d_scaled", turn)
+    monkeypatch.setattr(binding, "rope3d_scaled_bwd",
+                        lambda dq, dk=None, **kw: turn(dq, dk, -1.0, **kw))
+    q = torch.ones(1, 2, 8, 64, requires_grad=True)
+    for args in ((q, None), (q,)):
+        q.grad = None
+        got, none = autograd.rope3d(*args, grid=(1, 2, 4), bands=(8, 8, 8))
+        assert none is None
+        got.sum().backward()
+        assert bool((q.grad == -2.0).all())

@@ -3,7 +3,7 @@ a video DiT block for training.
 
     attention      binding.attention, differentiable in q, k, v through out and lse
     layer_norm     binding.layer_norm, differentiable in x, weight and bias
-    rope3d         binding.rope3d_scaled, differentiable in q and k
+    rope3d         binding.rope3d_scaled, differentiable in q (and k)
     qkv_attention  projection -> norm of q and k -> rotary embedding -> attention
                    as one function: the intermediate gradients stay in place
 
@@ -118,13 +118,15 @@ class _Rope(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dq, dk):
-        dq, dk = binding.rope3d_scaled_bwd(dq.contiguous(), dk.contiguous(), **ctx.turn)
+        dq, dk = binding.rope3d_scaled_bwd(dq.contiguous(), None if dk is None else dk.contiguous(),
+                                           **ctx.turn)
         return dq, dk, None
 
 
-def rope3d(q, k, **rope):
-    """binding.rope3d_scaled of q and k with gradients (options: grid, bands,
-    freqs or theta, pos_scale, amplitude, interleaved, token_offset)."""
+def rope3d(q, k=None, **rope):
+    """binding.rope3d_scaled of q (and k) with gradients (options: grid, bands,
+    freqs or theta, pos_scale, amplitude, interleaved, token_offset); returns
+    (q_rot, k_rot or None)."""
     return _Rope.apply(q, k, rope_arguments(rope))
 
 
