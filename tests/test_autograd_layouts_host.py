@@ -80,3 +80,28 @@ def test_rope_of_one_tensor(monkeypatch):
         assert none is None
         got.sum().backward()
         assert bool((q.grad == -2.0).all())
+
+
+def test_rope_options_are_taken_at_the_call(monkeypatch):
+    """What the caller changes in its lists between the forward and the backward
+    pass does not reach the gradient."""
+    seen = []
+
+    def turn(q, k=None, out_q=None, out_k=None, **turn):
+        seen.append({n: tuple(v) if n != "interleaved" else v for n, v in turn.items()})
+        return 1.0 * q, None
+
+    monkeypatch.setattr(binding, "rope3d_scaled", turn)
+    monkeypatch.setattr(binding, "rope3d_scaled_bwd", turn)
+    options = dict(grid=[1, 2, 4], bands=[8, 8, 8], freqs=[0.5] * 12, pos_scale=[1.0, 0.5, 1.0])
+    q = torch.ones(1, 2, 8, 64, requires_grad=True)
+    got, _ = autograd.rope3d(q, **options)
+    for v in options.values():
+        v[0] = 7
+    got.sum().backward()
+    assert seen[0] == seen[1] and seen[0]["freqs"] == (0.5,) * 12
+    freqs = torch.full((12,), 0.25)
+    got, _ = autograd.rope3d(q, grid=(1, 2, 4), bands=(8, 8, 8), freqs=freqs)
+    freqs.zero_()
+    got.sum().backward()
+    assert seen[2] == seen[3] and seen[3]["freqs"] == (0.25,) * 12

@@ -97,15 +97,21 @@ _TURN = ("grid", "bands", "freqs", "pos_scale", "amplitude", "interleaved", "tok
 
 def rope_arguments(rope):
     """rope3d_scaled's arguments from a dict of them, in which ``freqs`` may be
-    left out (theta's own frequencies, 10000 by default)."""
+    left out (theta's own frequencies, 10000 by default).  Sequences are copied:
+    a backward pass turns by what the forward was given."""
     unknown = set(rope) - set(_TURN) - {"theta"}
     if unknown:
         raise ValueError(f"unknown rope options: {sorted(unknown)}")
     turn = {n: rope[n] for n in _TURN if rope.get(n) is not None}
+    for n in ("grid", "bands", "pos_scale"):
+        if n in turn:
+            turn[n] = tuple(turn[n])
     if "freqs" not in turn:
         turn["freqs"] = binding.rope3d_frequencies(rope["bands"], rope.get("theta", 10000.0))
     elif "theta" in rope:
         raise ValueError("give freqs or theta, not both")
+    else:
+        turn["freqs"] = tuple(map(float, turn["freqs"]))
     return turn
 
 
