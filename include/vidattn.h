@@ -268,8 +268,7 @@ VIDATTN_API int vidattn_fwd_noalloc(const void* q, const void* k, const void* v,
 /*
  * vidattn_bwd — the gradient of vidattn_fwd_ex: from the gradients of its out
  * and lse, those of its q, k and v.  The softmax weights are recomputed tile
- * by tile from q, k and the forward's lse (after FlashAttention's backward
- * pass, the vidax paper's reference [2]); nothing quadratic in S is stored:
+ * by tile from q, k and the forward's lse; nothing quadratic in S is stored:
  *
  *   with P_ij = exp(scale * q_i . k_j - lse_i) for the keys j visible to query
  *   i (0 for the others), dP_ij = dout_i . v_j and
@@ -282,7 +281,8 @@ VIDATTN_API int vidattn_fwd_noalloc(const void* q, const void* k, const void* v,
  *           as given to the forward (same layouts, same rules)
  *   out, lse  as the forward returned them, bf16 [B,H,S_q,D], fp32 [B,H,S_q]
  *   dout    bf16 [B,H,S_q,D]: gradient of out, contiguous, 16-byte aligned
- *   dlse    fp32 [B,H,S_q]: gradient of lse, or NULL for zero
+ *   dlse    fp32 [B,H,S_q]: gradient of lse, or NULL for zero; not used where
+ *           a query sees no key (lse = -inf), so it may be anything there
  *   dq      bf16 [B,H,S_q,D], written; dk, dv bf16 [B,H,S_kv,D], written.
  *           None may overlap an input or another output.  A query that sees
  *           no key gets dq = 0; a key no query sees gets dk = dv = 0.
@@ -295,9 +295,10 @@ VIDATTN_API int vidattn_fwd_noalloc(const void* q, const void* k, const void* v,
  *           free once the stream has passed it.  Calls that may overlap on
  *           the GPU, or graphs that may run at the same time, need one each.
  *
- * Every value must be finite, padding's too (an infinity or a NaN in a token
- * may reach the gradients of all tokens of its 128-token tile, as in the
- * forward).  Arithmetic: products of bf16 values accumulated in fp32; P, dP,
+ * Every other value must be finite, padding's too (an infinity or a NaN in a
+ * token, or in a row of dout, may reach the gradients of all tokens of the
+ * 128-token tiles it meets, as in the forward; lse may be -inf as the forward
+ * left it).  Arithmetic: products of bf16 values accumulated in fp32; P, dP,
  * delta and dS = P (dP - delta) in fp32; P and dS are rounded to bf16 where
  * they enter a product (they are operands of the tensor core); each gradient
  * is summed in fp32 in a fixed order and rounded once to bf16.  The same

@@ -59,7 +59,8 @@ class _Attention(torch.autograd.Function):
 
 def attention(q, k, v, seg_q=None, seg_kv=None, scale=None, causal=False):
     """binding.attention with gradients; returns (out, lse).  Where a query sees
-    no key, out is 0, lse -inf, and both pass no gradient on."""
+    no key, out is 0, lse -inf, and both pass no gradient on: lse's may be an
+    infinity or a NaN there, out's has to be finite as everywhere."""
     return _Attention.apply(q, k, v, seg_q, seg_kv, scale, causal)
 
 

@@ -311,7 +311,7 @@ def attention_bwd(dout, q, k, v, out, lse, seg_q=None, seg_kv=None, scale=None, 
     """The gradients (dq, dk, dv) of ``attention``: dout is the gradient of its
     out, dlse (or None) that of its lse; out and lse are what it returned, the
     rest what it was given.  dout: bf16 [B,H,S_q,D] contiguous; dlse: fp32
-    [B,H,S_q].  n_split forces the split of long units (0: the library's
+    [B,H,S_q], not used where lse is -inf.  n_split forces the split of long units (0: the library's
     choice).  Returns bf16 tensors of the shapes of q, k, v; raises on error."""
     import torch
     _check_tensors(dict(q=q, k=k, v=v, dout=dout, out=out), torch.bfloat16, ndim=4)

@@ -42,8 +42,8 @@ constexpr int kBwdThreads = 640;   // 2 warps more: registers are dealt to 4 war
 constexpr int kBwdMaxListed = 2944;   // tiles of a unit's range whose visits are kept as bits
 
 struct BwdParams {
-  // per 128-row query tile: -lse * log2(e) (row sees nothing or is past S_q:
-  // -inf, so its P is 0) and -delta, fp32 [B*H][n_q_tiles][2][128]
+  // per 128-row query tile: -lse * log2(e) and -delta (row sees nothing or is
+  // past S_q: -inf and 0, so its P and dS are 0), fp32 [B*H][n_q_tiles][2][128]
   const float* stats;
   const int32_t* seg_q;     // [B,S_q] or null
   const int32_t* seg_kv;    // [B,S_kv] or null
@@ -822,7 +822,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 }
 
 // Ahead of the main kernel, one CTA per 128-row tile: -lse log2(e) and -delta
-// of a query tile of one (b, h) (blocks [0, BH * n_q_tiles)), and, with ids,
+// of a query tile of one (b, h) (blocks [0, BH * n_q_tiles); -inf and 0 for a
+// row that sees nothing), and, with ids,
 // the tile summaries {min, max, uniform, 0} of seg_q (by the blocks of head
 // 0) and seg_kv (the blocks behind).  delta = dout . out - dlse: one pass
 // over dout and out, 16 bytes a lane, D / 8 lanes a row.
@@ -869,8 +870,10 @@ __global__ void __launch_bounds__(256)
         float nl = -INFINITY, nd = 0.f;
         if (row < S_q) {
           const float l = __ldg(lse + at);
-          if (l != -INFINITY) nl = -l * 1.44269504088896341f;
-          nd = (dlse ? __ldg(dlse + at) : 0.f) - acc;
+          if (l != -INFINITY) {   // else dlse may be a NaN, which 0 P would keep
+            nl = -l * 1.44269504088896341f;
+            nd = (dlse ? __ldg(dlse + at) : 0.f) - acc;
+          }
         }
         st[r] = nl;
         st[128 + r] = nd;
