@@ -98,22 +98,41 @@ _TURN = ("grid", "bands", "freqs", "pos_scale", "amplitude", "interleaved", "tok
 
 def rope_arguments(rope):
     """rope3d_scaled's arguments from a dict of them, in which ``freqs`` may be
-    left out (theta's own frequencies, 10000 by default).  Sequences are copied:
-    a backward pass turns by what the forward was given."""
-    unknown = set(rope) - set(_TURN) - {"theta"}
+    left out (theta's own frequencies, 10000 by default) and ``token_offset``
+    may be called ``offset``; None stands for an option's default.  Sequences
+    are copied: a backward pass turns by what the forward was given."""
+    unknown = set(rope) - set(_TURN) - {"theta", "offset"}
     if unknown:
         raise ValueError(f"unknown rope options: {sorted(unknown)}")
-    turn = {n: rope[n] for n in _TURN if rope.get(n) is not None}
+    rope = {n: v for n, v in rope.items() if v is not None}
+    if "offset" in rope:
+        if "token_offset" in rope:
+            raise ValueError("give offset or token_offset, not both")
+        rope["token_offset"] = rope.pop("offset")
+    for n in ("grid", "bands"):
+        if n not in rope:
+            raise ValueError(f"rope needs {n}")
+    turn = {n: rope[n] for n in _TURN if n in rope}
     for n in ("grid", "bands", "pos_scale"):
         if n in turn:
             turn[n] = tuple(turn[n])
     if "freqs" not in turn:
-        turn["freqs"] = binding.rope3d_frequencies(rope["bands"], rope.get("theta", 10000.0))
+        turn["freqs"] = binding.rope3d_frequencies(turn["bands"], rope.get("theta", 10000.0))
     elif "theta" in rope:
         raise ValueError("give freqs or theta, not both")
     else:
         turn["freqs"] = tuple(map(float, turn["freqs"]))
     return turn
+
+
+def norm_arguments(qk_norm):
+    """(weight, bias) of q, (weight, bias) of k and eps from a qk_norm dict."""
+    unknown = set(qk_norm) - {"q", "k", "eps"}
+    if unknown:
+        raise ValueError(f"unknown qk_norm options: {sorted(unknown)}")
+    eps = qk_norm.get("eps")
+    return (qk_norm.get("q") or (None, None), qk_norm.get("k") or (None, None),
+            1e-6 if eps is None else eps)
 
 
 class _Rope(torch.autograd.Function):
@@ -190,14 +209,9 @@ def qkv_attention(q, k, v, qk_norm=None, rope=None, seg_q=None, seg_kv=None, sca
     wq = bq = wk = bk = None
     eps = 1e-6
     if qk_norm is not None:
-        unknown = set(qk_norm) - {"q", "k", "eps"}
-        if unknown:
-            raise ValueError(f"unknown qk_norm options: {sorted(unknown)}")
-        wq, bq = qk_norm.get("q") or (None, None)
-        wk, bk = qk_norm.get("k") or (None, None)
+        (wq, bq), (wk, bk), eps = norm_arguments(qk_norm)
         _check_bias(wq, bq)
         _check_bias(wk, bk)
-        eps = qk_norm.get("eps", 1e-6)
     turn = None if rope is None else rope_arguments(rope)
     return _QkvAttention.apply(q, k, v, wq, bq, wk, bk, eps, turn, seg_q, seg_kv, scale, causal,
                                qk_norm is not None)

@@ -34,6 +34,7 @@ import torch
 import torch.distributed as dist
 
 from . import binding
+from .autograd import norm_arguments, rope_arguments
 
 
 def _world(group):
@@ -126,17 +127,18 @@ def _cuda_norm(x, weight, bias, eps):
     return binding.layer_norm(x, weight, bias, eps)[0]
 
 
-def _cuda_rope(q, k, rope):
+def _cuda_rope(rope, D):
+    """The rotation by these options, checked once, as rope_fn is called."""
+    turn = rope_arguments(rope)
     # out of place: without an exchange (one rank) q and k are views of the
     # caller's tensors, which must not change
-    if rope.get("freqs") is not None:
-        return binding.rope3d_scaled(q, k, rope["grid"], rope["bands"], rope["freqs"],
-                                     rope.get("pos_scale", (1.0, 1.0, 1.0)),
-                                     rope.get("amplitude", 1.0), rope.get("interleaved", True),
-                                     rope.get("offset", 0))
-    return binding.rope3d(q, k, rope["grid"], rope["bands"], theta=rope.get("theta", 10000.0),
-                          interleaved=rope.get("interleaved", True),
-                          token_offset=rope.get("offset", 0))
+    if any(rope.get(n) is not None for n in ("freqs", "pos_scale", "amplitude")) or \
+            sum(turn["bands"]) != D:
+        return lambda q, k, _: binding.rope3d_scaled(q, k, **turn)
+    theta = 10000.0 if rope.get("theta") is None else rope["theta"]
+    return lambda q, k, _: binding.rope3d(q, k, turn["grid"], turn["bands"], theta=theta,
+                                          interleaved=turn.get("interleaved", True),
+                                          token_offset=turn.get("token_offset", 0))
 
 
 def _all_gather_seq(x, P, group):
@@ -158,8 +160,9 @@ def ulysses_attention(q, k, v, seg=None, scale=None, causal=False, group=None, n
     [B, S/P] packed t << 22 | h << 11 | w of this rank's tokens, size, extent,
     clamped) for 3D neighbourhood attention, or None.  rope: dict(grid, bands,
     theta, interleaved, offset) to rotate q and k (global positions) before
-    the attention, or None; with freqs (and pos_scale, amplitude) in the place
-    of theta, as binding.rope3d_scaled takes them.  qk_norm: dict(q=(weight,
+    the attention, or None; with freqs in the place of theta, pos_scale and
+    amplitude, and bands over a part of the head, as autograd.rope3d takes them
+    (offset is its token_offset).  qk_norm: dict(q=(weight,
     bias), k=(weight, bias), eps) to layer-norm q and k over each head ahead of
     both, weight and bias [D] or None, or None.  Returns (out [B, H, S/P, D], lse fp32 [B, H, S/P])
     for this rank's shard, equal to the corresponding rows of single-device
@@ -174,13 +177,14 @@ def ulysses_attention(q, k, v, seg=None, scale=None, causal=False, group=None, n
         scale = D ** -0.5
     if window is not None and (seg is not None or causal):
         raise ValueError("a window goes without ids and without the causal limit")
+    turn = rope_fn
+    if rope is not None and turn is None:
+        turn = _cuda_rope(rope, D)
     if qk_norm is not None:
         norm = norm_fn or _cuda_norm
-        eps = qk_norm.get("eps", 1e-6)
-        q = norm(q, *(qk_norm.get("q") or (None, None)), eps)
-        k = norm(k, *(qk_norm.get("k") or (None, None)), eps)
+        of_q, of_k, eps = norm_arguments(qk_norm)
+        q, k = norm(q, *of_q, eps), norm(k, *of_k, eps)
     attn = attn_fn or _cuda_attention
-    turn = rope_fn or _cuda_rope
     seg_full = None if seg is None else _all_gather_seq(seg, P, group)
     win_full = None
     if window is not None:
