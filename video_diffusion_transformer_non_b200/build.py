@@ -23,7 +23,8 @@ PROBES_OUT = os.path.join(CSRC, "libvidattn_probes.so")
 TARGETS = [
     (OUT, ["vidattn.cu", "bwd.cu", "norm.cu"],
      ["vidattn.cu", "fwd_kernel.cuh", "classify.cuh", "ptx.cuh", "rope3d.cuh", "internal.h",
-      "bwd.cu", "bwd_kernel.cuh", "norm.cu", "layernorm.cuh", "ptx_train.cuh"]),
+      "bwd.cu", "bwd_kernel.cuh", "norm.cu", "layernorm.cuh", "ptx_train.cuh",
+      "bounded_wait.h"]),
     # unit probes of the kernel's tensor-core steps, used only by the GPU tests
     (PROBES_OUT, ["probes.cu"], ["probes.cu", "fwd_kernel.cuh", "ptx.cuh"]),
 ]

@@ -32,6 +32,7 @@
 #include <cstdint>
 #include <cuda.h>
 
+#include "bounded_wait.h"
 #include "ptx_train.cuh"
 
 namespace vidattn {
@@ -196,21 +197,24 @@ constexpr uint64_t kBwdWaitTimeoutNs = 2000000000ull;
 constexpr int kBwdErrTimeout = 1;   // bit of the device error word, as the forward's
 static __device__ __noinline__ bool bwd_wait_slow(uint32_t bar, uint32_t parity,
                                                   volatile int* abort_flag, int* err) {
-  uint64_t t0 = 0;
-  bool ok = mbar_try_wait(bar, parity);
-  for (uint32_t it = 1; !ok; ++it) {
-    ok = mbar_try_wait(bar, parity);
-    if (ok || (it & 255u) != 0) continue;
-    // give up at once if this CTA, or any CTA of this launch, already did
-    const bool gone = *abort_flag != 0 || *reinterpret_cast<volatile int*>(err) != 0;
-    const uint64_t now = globaltimer_ns();
-    if (t0 == 0) t0 = now;
-    if (!gone && now - t0 <= kBwdWaitTimeoutNs) continue;
-    *abort_flag = 1;
-    if (!gone) atomicOr(err, kBwdErrTimeout);
-    break;
-  }
-  return __all_sync(0xffffffffu, ok);
+  const WaitEnd end = bounded_wait<false>(
+      [&] { return mbar_try_wait(bar, parity); },
+      [&] { return *abort_flag != 0 || *reinterpret_cast<volatile int*>(err) != 0; },
+      [] { return globaltimer_ns(); }, kBwdWaitTimeoutNs);
+  if (end != WaitEnd::kPhase) *abort_flag = 1;
+  if (end == WaitEnd::kTimeout) atomicOr(err, kBwdErrTimeout);
+  return __all_sync(0xffffffffu, end == WaitEnd::kPhase);
+}
+// The wait for loads or products in flight ahead of the CTA's end (a converged
+// warp): it ends at their phase or at the time limit from `since`, not with a
+// wait that ran out elsewhere.
+static __device__ __noinline__ void bwd_drain(uint32_t bar, uint32_t parity, int* err,
+                                              uint64_t since) {
+  const WaitEnd end = bounded_wait<true>([&] { return mbar_try_wait(bar, parity); },
+                                         [] { return false; }, [] { return globaltimer_ns(); },
+                                         kBwdWaitTimeoutNs, since);
+  if (end == WaitEnd::kTimeout) atomicOr(err, kBwdErrTimeout);
+  __syncwarp();
 }
 __device__ __forceinline__ bool bwd_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                          int* err) {
@@ -548,17 +552,14 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
         if (ok) load(n, walk.first + pos, which);
       }
     }
-    if (!ok) {
-      // let the loads in flight land before the CTA can exit (a wait ends at
-      // the phase of its load, or by its time limit)
-      volatile int never = 0;
-      for (int k = max(0, n_a - kA); k < n_a; ++k)
-        bwd_wait_slow(a_full(k), a_par(k), &never, p.err);
-      for (int k = max(0, n_b - kB); k < n_b; ++k)
-        bwd_wait_slow(b_full(k), b_par(k), &never, p.err);
-      for (int which = 0; which < 2; ++which)
-        bwd_wait_slow(fixed_full(which), 0, &never, p.err);
-    }
+    // Every load has landed before the CTA can exit: where all went well the
+    // products have waited for it, but this warp may have issued its last load
+    // when another gave up.
+    const uint64_t since = globaltimer_ns();
+    for (int k = max(0, n_a - kA); k < n_a; ++k) bwd_drain(a_full(k), a_par(k), p.err, since);
+    for (int k = max(0, n_b - kB); k < n_b; ++k) bwd_drain(b_full(k), b_par(k), p.err, since);
+    for (int which = 0; which < 2 && n_tiles > 0; ++which)
+      bwd_drain(fixed_full(which), 0, p.err, since);
     __syncwarp();
   } else if (warp == kBwdMmaWarp) {
     // -------------------------------------------------------- tensor core
@@ -619,9 +620,7 @@ __device__ __forceinline__ void bwd_unit(const CUtensorMap& tm_q, const CUtensor
     // every product issued has finished before the epilogue and the release
     // of tensor memory
     mma_commit_elect(done);
-    volatile int never = 0;
-    bwd_wait_slow(done, 0, &never, p.err);
-    __syncwarp();
+    bwd_drain(done, 0, p.err, globaltimer_ns());
   } else if (warp < kBwdSoftmaxWarps) {
     // --------------------------------------------------------- P and dS
     const int quarter = warp >> 2;   // of a tile's columns
@@ -766,8 +765,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t sbase = smem_u32(smem_raw);
   uint8_t* smem = smem_raw;
-  // a wait of an earlier CTA timed out: the results are already invalid
-  if (*reinterpret_cast<volatile int*>(p.err) != 0) return;
+  // a wait of an earlier CTA timed out: the results are already invalid.  One
+  // thread's look decides for all: the word may change between two.
+  if (__syncthreads_or(threadIdx.x == 0 && *reinterpret_cast<volatile int*>(p.err) != 0)) return;
   if (sbase & 1023u) {   // the tiles' swizzle needs the alignment asked for above
     if (threadIdx.x == 0) atomicOr(p.err, kBwdErrTimeout);
     return;
