@@ -311,8 +311,8 @@ def attention_bwd(dout, q, k, v, out, lse, seg_q=None, seg_kv=None, scale=None, 
     """The gradients (dq, dk, dv) of ``attention``: dout is the gradient of its
     out, dlse (or None) that of its lse; out and lse are what it returned, the
     rest what it was given.  dout: bf16 [B,H,S_q,D] contiguous; dlse: fp32
-    [B,H,S_q], not used where lse is -inf.  n_split forces the split of long units (0: the library's
-    choice).  Returns bf16 tensors of the shapes of q, k, v; raises on error."""
+    [B,H,S_q], not used where lse is -inf.  n_split (1 to 64) forces the split of units (0: the
+    library's choice).  Returns bf16 tensors of the shapes of q, k, v; raises on error."""
     import torch
     _check_tensors(dict(q=q, k=k, v=v, dout=dout, out=out), torch.bfloat16, ndim=4)
     _check_tensors(dict(lse=lse, dlse=dlse), torch.float32, ndim=3)
@@ -326,6 +326,8 @@ def attention_bwd(dout, q, k, v, out, lse, seg_q=None, seg_kv=None, scale=None, 
     if lse.device != q.device:
         raise ValueError(f"lse is on {lse.device}, q on {q.device}")
     _check_per_token("seg_q", seg_q, "seg_kv", seg_kv, B, S_q, S_kv, q.device)
+    if not 0 <= n_split <= 64:
+        raise ValueError(f"n_split must be 0 to 64 (is {n_split})")
     if scale is None:
         scale = D ** -0.5
     flags = (VIDATTN_CAUSAL if causal else 0) | VIDATTN_SPLIT_KV(n_split)
