@@ -91,6 +91,16 @@ BwdPlan bwd_plan(bool ids, int B, int H, int S_q, int S_kv, int D, int flags) {
   return r;
 }
 
+// Do the grids of the kernels hold a call of these sizes (checked otherwise)?
+bool bwd_fits(bool ids, int B, int H, int S_q, int S_kv, int D, int flags) {
+  if (S_q == 0 || S_kv == 0) return true;   // no kernel runs
+  const int64_t BH = int64_t(B) * H;
+  if (BH * tiles(S_q) > INT_MAX || BH * tiles(S_kv) > INT_MAX) return false;
+  const BwdPlan plan = bwd_plan(ids, B, H, S_q, S_kv, D, flags);
+  return BH * plan.n_kv * plan.kv_split + BH * plan.n_q * plan.q_split <= INT_MAX &&
+         BH * plan.n_q + (ids ? int64_t(B) * plan.n_kv : 0) <= INT_MAX;
+}
+
 // Raises the kernels' shared-memory limit once per device (and again after
 // vidattn_release).
 std::mutex g_bwd_mu;
@@ -130,7 +140,8 @@ VIDATTN_API int64_t vidattn_bwd_workspace(int has_ids, int B, int H, int S_q, in
                                           int flags) {
   if (B < 1 || H < 1 || B > 65535 || H > 65535 || S_q < 0 || S_kv < 0 || (D != 64 && D != 128) ||
       (flags & ~(VIDATTN_CAUSAL | VIDATTN_SPLIT_KV(0xFF))) ||
-      ((flags >> 8) & 0xFF) > kBwdMaxSplit || S_q > INT_MAX - 256 || S_kv > INT_MAX - 256)
+      ((flags >> 8) & 0xFF) > kBwdMaxSplit || S_q > INT_MAX - 256 || S_kv > INT_MAX - 256 ||
+      !bwd_fits(has_ids != 0, B, H, S_q, S_kv, D, flags))
     return -1;
   return int64_t(bwd_plan(has_ids != 0, B, H, S_q, S_kv, D, flags).bytes);
 }
@@ -149,7 +160,8 @@ VIDATTN_API int vidattn_bwd(const void* q, const void* k, const void* v, const v
   if ((seg_q == nullptr) != (seg_kv == nullptr)) return VIDATTN_ERR_SEG_PAIR;
   if (D != 64 && D != 128) return VIDATTN_ERR_UNSUPPORTED_D;
   if (B < 1 || H < 1 || B > 65535 || H > 65535 || S_q < 0 || S_kv < 0 || S_q > INT_MAX - 256 ||
-      S_kv > INT_MAX - 256 || !std::isfinite(scale))
+      S_kv > INT_MAX - 256 || !std::isfinite(scale) ||
+      !bwd_fits(seg_q != nullptr, B, H, S_q, S_kv, D, flags))
     return VIDATTN_ERR_BAD_SHAPE;
   for (const void* p : {q, k, v, out, dout, static_cast<const void*>(dq),
                         static_cast<const void*>(dk), static_cast<const void*>(dv)})
@@ -165,7 +177,6 @@ VIDATTN_API int vidattn_bwd(const void* q, const void* k, const void* v, const v
   if (S_q > 0 && S_kv > 0) {
     if (!workspace) return VIDATTN_ERR_NULL;
     if (workspace_bytes < int64_t(plan.bytes)) return VIDATTN_ERR_SCRATCH_LIMIT;
-    if (n_units > INT_MAX) return VIDATTN_ERR_BAD_SHAPE;
   }
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   int dev = 0, sms = 0;
@@ -192,7 +203,6 @@ VIDATTN_API int vidattn_bwd(const void* q, const void* k, const void* v, const v
   int4* q_sum = seg_q ? reinterpret_cast<int4*>(ws + plan.sums) : nullptr;
   int4* kv_sum = seg_q ? q_sum + size_t(B) * plan.n_q : nullptr;
   const int64_t prep = BH * plan.n_q + (seg_q ? int64_t(B) * plan.n_kv : 0);
-  if (prep > INT_MAX) return VIDATTN_ERR_BAD_SHAPE;
   auto prepare = D == 128 ? launch_prepare<128> : launch_prepare<64>;
   prepare(out, dout, lse, dlse, seg_q, seg_kv, stats, q_sum, kv_sum, prep, int(BH), H, S_q, S_kv,
           plan.n_q, plan.n_kv, stream);
