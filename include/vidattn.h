@@ -340,7 +340,8 @@ VIDATTN_API int64_t vidattn_bwd_workspace(int has_ids, int B, int H, int S_q, in
  *            h*x_strides[1] + s*x_strides[2] + f; strides in elements, >= 0
  *   weight, bias  [N] of param_type (bf16 or fp32), either may be NULL (1, 0)
  *   y        as x, with strides of its own; its rows must not overlap.  x
- *            itself with x's strides (in place), or memory apart from x.
+ *            itself with x's strides (in place; with others BAD_SHAPE), or
+ *            memory apart from x.
  *   mean, rstd  fp32 [B,H,S] contiguous, written; either may be NULL
  *   B, H >= 1; S >= 0; 1 <= N <= 16384; B*H*S < 2^31; eps >= 0, finite.
  *
@@ -368,7 +369,7 @@ VIDATTN_API int vidattn_layernorm(const void* x, const void* weight, const void*
  *   mean, rstd  as the forward wrote them
  *   weight   as given to the forward, or NULL
  *   dx       as x, strides of its own, rows apart; x or dy itself with the
- *            same strides, or memory apart from both
+ *            same strides (with others BAD_SHAPE), or memory apart from both
  *   dweight, dbias  [N] of param_type, written; either may be NULL
  *   workspace  vidattn_layernorm_bwd_workspace(...) bytes, 256-byte aligned,
  *            the caller's, for this call alone until the stream has passed it;

@@ -1,0 +1,24 @@
+"""Calls whose outputs lie over an input in another layout, or over the other
+tensor: the kernels would read what they have written.  Refused at the C entry
+points before anything is enqueued, and so in the binding; no GPU."""
+import pytest
+
+from test_norm_rope_host import A, codes, ln, ln_bwd   # noqa: F401
+
+X = (1920, 640, 64)          # [2,3,10,64] contiguous
+T = (1920, 64, 192)          # a [2,10,3,64] projection's transpose
+B = A + (1 << 16)            # memory of its own
+
+
+@pytest.mark.parametrize("kw,name", [
+    (dict(sx=X, sy=T), "BAD_SHAPE"), (dict(sx=T, sy=X), "BAD_SHAPE"),
+    (dict(sx=(0, 640, 64), sy=X), "BAD_SHAPE")])
+def test_norm_over_its_input_in_another_layout(codes, kw, name):
+    assert ln(x=A, y=A, **kw) == codes[name]
+
+
+@pytest.mark.parametrize("kw", [
+    dict(x=A, dy=B, sx=X, sdy=X, sdx=T), dict(x=B, dy=A, sx=X, sdy=X, sdx=T),
+    dict(x=B, dy=A, sx=T, sdy=T, sdx=X), dict(x=A, dy=A, sx=X, sdy=T, sdx=X)])
+def test_norm_gradient_over_an_input_in_another_layout(codes, kw):
+    assert ln_bwd(dx=A, **kw) == codes["BAD_SHAPE"]

@@ -41,5 +41,15 @@ inline bool rows_apart(const int64_t sizes[3], const int64_t strides[3], int64_t
   return true;
 }
 
+// An output over its own input: only with the input's strides (of the axes that
+// have any extent), else some rows are written before they are read.
+inline bool over_another_layout(const void* in, const void* out, const int64_t sizes[3],
+                                const int64_t in_strides[3], const int64_t out_strides[3]) {
+  if (in != out) return false;
+  for (int i = 0; i < 3; ++i)
+    if (sizes[i] > 1 && in_strides[i] != out_strides[i]) return true;
+  return false;
+}
+
 }  // namespace host
 }  // namespace vidattn

@@ -112,6 +112,11 @@ bool ln_apart(int B, int H, int S, int N, const int64_t s[3]) {
   const int64_t sizes[3] = {B, H, S};
   return host::rows_apart(sizes, s, N);
 }
+bool ln_in_place_ok(const void* in, const void* out, int B, int H, int S, const int64_t si[3],
+                    const int64_t so[3]) {
+  const int64_t sizes[3] = {B, H, S};
+  return !host::over_another_layout(in, out, sizes, si, so);
+}
 // Any read layout: strides not negative.
 bool ln_readable(const int64_t s[3]) { return s[0] >= 0 && s[1] >= 0 && s[2] >= 0; }
 bool ln_on(const void* p, const int64_t s[3], int item, int bytes) {
@@ -149,6 +154,7 @@ VIDATTN_API int vidattn_layernorm(const void* x, const void* weight, const void*
     return VIDATTN_ERR_BAD_SHAPE;
   if (S == 0) return VIDATTN_OK;
   if (!x || !y) return VIDATTN_ERR_NULL;
+  if (!ln_in_place_ok(x, y, B, H, S, x_strides, y_strides)) return VIDATTN_ERR_BAD_SHAPE;
   const int item = ln_item(x_type), pitem = ln_item(param_type);
   if (!host::aligned(x, item) || !host::aligned(y, item) || !host::aligned(weight, pitem) ||
       !host::aligned(bias, pitem) || !host::aligned(mean, 4) || !host::aligned(rstd, 4))
@@ -209,6 +215,9 @@ VIDATTN_API int vidattn_layernorm_bwd(const void* dy, const void* x, const float
   const bool params = dweight || dbias;
   if (S > 0 && (!dy || !x || !mean || !rstd || !dx || (params && !workspace)))
     return VIDATTN_ERR_NULL;
+  if (S > 0 && (!ln_in_place_ok(x, dx, B, H, S, x_strides, dx_strides) ||
+                !ln_in_place_ok(dy, dx, B, H, S, dy_strides, dx_strides)))
+    return VIDATTN_ERR_BAD_SHAPE;
   if (!host::aligned(x, item) || !host::aligned(dy, item) || !host::aligned(dx, item) ||
       !host::aligned(weight, pitem) || !host::aligned(dweight, pitem) ||
       !host::aligned(dbias, pitem) || !host::aligned(mean, 4) || !host::aligned(rstd, 4) ||
