@@ -473,7 +473,9 @@ VIDATTN_API int vidattn_rope3d(const void* q_in, const void* k_in, void* q_out, 
  *   in_strides, out_strides  3 strides each (batch, head, token) in elements,
  *              multiples of 8, of q_in and k_in and of q_out and k_out; input
  *              strides >= 0; output rows apart.  An output is its input (then
- *              with the same strides) or memory apart from both inputs.
+ *              with the same strides) or memory apart from both inputs and from
+ *              the other output; BAD_SHAPE where one starts on another tensor,
+ *              or on its input with other strides.
  *   flags      VIDATTN_ROPE_HALF_SPLIT | VIDATTN_ROPE_TRANSPOSE
  *   the rest   as vidattn_rope3d
  *

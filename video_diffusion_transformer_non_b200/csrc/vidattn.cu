@@ -1024,6 +1024,10 @@ VIDATTN_API int vidattn_rope3d_scaled(const void* q_in, const void* k_in, void* 
     if (in_strides[i] % 8 || out_strides[i] % 8) return VIDATTN_ERR_MISALIGNED;
   }
   if (!host::rows_apart(sizes, out_strides, D)) return VIDATTN_ERR_BAD_SHAPE;
+  if (host::over_another_layout(q_in, q_out, sizes, in_strides, out_strides) ||
+      (k_in && (host::over_another_layout(k_in, k_out, sizes, in_strides, out_strides) ||
+                q_out == k_out || q_out == k_in || k_out == q_in)))
+    return VIDATTN_ERR_BAD_SHAPE;
   int dev = 0;
   st = ensure_device(&dev);
   if (st != VIDATTN_OK) return st;
