@@ -75,7 +75,8 @@ __device__ __forceinline__ uint16_t ln_to_bf16(float v) {
 }
 
 // Turns of the ring: up to 4 in 192 KB, or in 64 KB where several CTAs fit an SM
-// (fewer than 2: rows go through registers).
+// (fewer than 2, backward with fp32 rows of more than 8192: they go through
+// registers).
 __host__ __device__ constexpr int ln_stages(int threads, int rows, int tensors, int bytes_a_thread) {
   const int stage = threads * rows * tensors * bytes_a_thread;
   int n = (threads <= 512 ? 65536 : 196608) / stage;
@@ -128,15 +129,14 @@ struct LnFrag {
   }
   // Features at and behind N read as 0.
   __device__ __forceinline__ void load(const X* row, int lane, int lanes, int N) {
+    static_assert(!kOdd, "only rows of fp32 go without the ring");
     clear();
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int at = (i * lanes + lane) * kCols;
       if (at >= N) continue;
       uint32_t* d = r + i * (kWords / kPieces);
-      if constexpr (kOdd) {
-        d[0] = uint32_t(row[at]) | (at + 1 < N ? uint32_t(row[at + 1]) << 16 : 0u);
-      } else if constexpr (kPieceBytes == 16) {
+      if constexpr (kPieceBytes == 16) {
         const uint4 v = *reinterpret_cast<const uint4*>(row + at);
         d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
       } else {
@@ -341,8 +341,9 @@ template <typename X, int kLanes, int kC, int kR, int kV, int kMaxThreads, int k
 __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_fwd_kernel(const LnParams p) {
   using Walk = LnWalk<X, kLanes, kC, kR, kV, kMaxThreads, 1>;
   using Frag = typename Walk::Frag;
-  constexpr bool kBlock = Walk::kBlock, kRing = Walk::kRing;
+  constexpr bool kBlock = Walk::kBlock;
   constexpr int kE = 8 * kC, kS = Walk::kS;
+  static_assert(kS >= 2, "every forward form has a ring");
   __shared__ __align__(16) float buf[kBlock ? 4 : 1][kR][32];
   if (kBlock) {
     for (int i = threadIdx.x; i < 4 * kR * 32; i += blockDim.x) (&buf[0][0][0])[i] = 0.f;
@@ -352,52 +353,33 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_fwd_kernel(const LnPara
   const int lane = t.lane, lanes = t.lanes;
   const X* x = static_cast<const X*>(p.x);
   X* y = static_cast<X*>(p.y);
-  Frag next[kRing ? 1 : kR];
   auto fetch = [&](uint32_t row0) {
 #pragma unroll
     for (int i = 0; i < kR; ++i) {
       const uint32_t row = row0 + i * t.groups;
-      if constexpr (kRing) {
-        if (row < p.rows)
-          Frag::copy(t.slot(t.in, i, 0), t.pitch, x + ln_offset(p, p.lx, row), lane, lanes,
-                     p.N);
-      } else {
-        if (row < p.rows) next[i].load(x + ln_offset(p, p.lx, row), lane, lanes, p.N);
-        else next[i].clear();
-      }
+      if (row < p.rows)
+        Frag::copy(t.slot(t.in, i, 0), t.pitch, x + ln_offset(p, p.lx, row), lane, lanes, p.N);
     }
-    if constexpr (kRing) {
-      t.next(t.in);
-      ln_commit();
-    }
+    t.next(t.in);
+    ln_commit();
   };
-  if constexpr (kRing) {
 #pragma unroll
-    for (int k = 0; k < kS - 1; ++k) fetch(t.row + k * t.step);
-  } else {
-    fetch(t.row);
-  }
+  for (int k = 0; k < kS - 1; ++k) fetch(t.row + k * t.step);
   float2 w[kE / 2], b[kE / 2];
   ln_params<kC, Frag::kCols>(p.w, p.params_bf16, lane, lanes, p.N, 1.f, w);
   ln_params<kC, Frag::kCols>(p.b, p.params_bf16, lane, lanes, p.N, 0.f, b);
   for (int turn = 0; t.any(p); turn ^= 1, t.row += t.step) {
     Frag cur[kR];
-    if constexpr (kRing) {
-      fetch(t.row + (kS - 1) * t.step);
-      ln_wait<kRing ? kS - 1 : 0>();
-      if (Frag::kOdd) kBlock ? __syncthreads() : __syncwarp();
+    fetch(t.row + (kS - 1) * t.step);
+    ln_wait<kS - 1>();
+    if (Frag::kOdd) kBlock ? __syncthreads() : __syncwarp();
 #pragma unroll
-      for (int i = 0; i < kR; ++i) {
-        const uint32_t row = min(t.row + i * t.groups, uint32_t(p.rows - 1));
-        cur[i].read(t.slot(t.out, i, 0), t.pitch,
-                    Frag::kOdd ? x + ln_offset(p, p.lx, row) : nullptr, lane, lanes, p.N);
-      }
-      t.next(t.out);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kR; ++i) cur[i] = next[i];
-      if (kBlock) fetch(t.row + t.step);
+    for (int i = 0; i < kR; ++i) {
+      const uint32_t row = min(t.row + i * t.groups, uint32_t(p.rows - 1));
+      cur[i].read(t.slot(t.out, i, 0), t.pitch,
+                  Frag::kOdd ? x + ln_offset(p, p.lx, row) : nullptr, lane, lanes, p.N);
     }
+    t.next(t.out);
     float mean[kR], var[kR];
     float2 d[kR][kE / 2];
 #pragma unroll
@@ -442,7 +424,6 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_fwd_kernel(const LnPara
         }
       }
     }
-    if (!kRing && !kBlock) fetch(t.row + t.step);
   }
 }
 
@@ -452,6 +433,7 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_bwd_kernel(const LnPara
   using Frag = typename Walk::Frag;
   constexpr bool kBlock = Walk::kBlock, kRing = Walk::kRing;
   constexpr int kE = 8 * kC, kS = Walk::kS;
+  static_assert(kRing || kBlock, "only the longest rows go without the ring");
   // xh and g are kept from the sums to the result where registers allow
   constexpr bool kKeep = kC == 1 && kR <= 2 && kMaxThreads <= 320;
   __shared__ __align__(16) float buf[kBlock ? 2 : 1][2 * kR][32];
@@ -558,7 +540,7 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_bwd_kernel(const LnPara
     } else {
 #pragma unroll
       for (int i = 0; i < kR; ++i) cx[i] = nx[i], cg[i] = ng[i];
-      if (kBlock) fetch(t.row + t.step);
+      fetch(t.row + t.step);
     }
     float2 kx[kKeep ? kR : 1][kKeep ? kE / 2 : 1], kg[kKeep ? kR : 1][kKeep ? kE / 2 : 1];
 #pragma unroll
@@ -596,7 +578,6 @@ __global__ void __launch_bounds__(kMaxThreads, kCtas) ln_bwd_kernel(const LnPara
         ln_store<X, kC, kV>(dx + ln_offset(p, p.ly, row), lane, lanes, p.N, v);
       }
     }
-    if (!kRing && !kBlock) fetch(t.row + t.step);
   }
   if (p.part == nullptr) return;
   // this CTA's sums: the groups of a warp by shuffles, its warps in order
