@@ -69,7 +69,8 @@ typedef enum {
   VIDATTN_ERR_TIMEOUT = 6,         /* a kernel wait exceeded its time limit (device_status) */
   VIDATTN_ERR_NO_DEVICE = 7,       /* the current device is not sm_100 */
   VIDATTN_ERR_SEG_PAIR = 8,        /* exactly one of seg_q, seg_kv is NULL */
-  VIDATTN_ERR_SCRATCH_LIMIT = 9    /* vidattn_fwd_noalloc: shape exceeds its fixed scratch */
+  VIDATTN_ERR_SCRATCH_LIMIT = 9    /* vidattn_fwd_noalloc: shape exceeds its fixed scratch;
+                                      * a backward pass: its workspace is too small */
 } vidattn_status;
 
 /*

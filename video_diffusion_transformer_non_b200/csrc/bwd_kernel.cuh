@@ -21,8 +21,8 @@
 // (warp w: TMEM lanes 32 (w % 4) + [0, 32), columns 32 (w / 4) + [0, 32)); warp
 // 16 issues the tcgen05.mma, warp 17 the TMA loads.
 //
-// Measured (B200): 8 heads of 32760 x 128 in 11.0 ms, 8 x 32760^2 pairs at 998
-// TFLOP/s counting five products, 1397 counting the seven it does: the tensor
+// Measured (B200): 8 heads of 32760 x 128 in 11.25 ms, 8 x 32760^2 pairs at 977
+// TFLOP/s counting five products, 1368 counting the seven it does: the tensor
 // core's sustained rate under the power cap.  A tile pair takes 1.48 us in a KV
 // unit and 1.09 in a Q unit there; D = 64 takes 1.0 and 0.83, bound by the
 // exponentials and issue slots.  A unit's set-up, first loads, drain and stores

@@ -20,14 +20,15 @@
 // bf16 rows on odd places or of odd length are put together from 4-byte pieces
 // of neighbouring lanes, with a barrier a turn.
 //
-// Measured (B200): 32760 rows of 5120 bf16 in 112 us (6.0 TB/s, 91 % of the
-// copy rate), backward 193 us (5.2 TB/s); 524160 rows of 128, backward, from a
-// [B,S,H,D] projection 74 us (5.5 TB/s).  16000 rows, forward and backward: of
-// 5118 bf16 (pieces of 4 bytes) 88 and 152 us, of 5119 (odd) 135 and 237, of
-// 5120 fp32 116 and 178, of 5119 fp32 147 and 227; feature by feature through
-// registers the bf16 ones took 258 and 572.  Instruction issue bounds it (51 -
-// 64 % of the slots); a deeper ring, one CTA of twice the threads or 32
-// features a thread were slower.
+// Measured (B200): 32760 rows of 5120 bf16 in 113 us (5.9 TB/s, 91 % of the
+// copy rate), backward 196 us (5.1 TB/s); 524160 rows of 128 in 55 us (4.9 TB/s),
+// backward, from a [B,S,H,D] projection, 74 - 78 us (5.2 - 5.5 TB/s).  16000 rows,
+// forward and backward: of 8192 bf16 113 and 164 us, of 5118 (pieces of 4 bytes)
+// 90 and 154, of 5119 (odd) 135 and 238, of 5120 fp32 119 and 178, of 5119 fp32
+// 148 and 227; 8000 rows of 16384: bf16 125 and 285, fp32 173 and 657 (backward
+// without the ring).  Feature by feature through registers the rows of 5119 bf16
+// took 258 and 572.  Instruction issue bounds it (51 - 64 % of the slots); a deeper
+// ring, one CTA of twice the threads or 32 features a thread were slower.
 #pragma once
 #include <cuda_runtime.h>
 
