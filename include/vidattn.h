@@ -100,7 +100,11 @@ typedef enum {
  * (16 bytes per 128 tokens of seg_q and seg_kv), allocated on first use,
  * grown when a larger shape arrives (growing synchronises that stream), and
  * freed by vidattn_release().  Calls on one stream are ordered, so they never
- * share scratch in flight.
+ * share scratch in flight.  A buffer that a graph was captured with is kept
+ * until vidattn_release() when it is outgrown, so the graph stays valid; graphs
+ * captured on one stream share its scratch, so those that use it may not be
+ * replayed at the same time as one another or as calls on that stream (capture
+ * them on streams of their own).
  *
  * Errors: argument errors return their status before anything is enqueued;
  * launch failures return VIDATTN_ERR_CUDA.  S_q == 0 (with the other

@@ -13,7 +13,9 @@ backward pass.
 
 Inside a CUDA graph, capture forward and backward together, or use tensors
 whose gradients no eager graph still holds: torch's accumulation of a leaf's
-gradient runs on the stream that the leaf was first used on.
+gradient runs on the stream that the leaf was first used on.  The attention's
+forward pass keeps scratch per stream where it has ids or splits its keys: graphs
+that may be replayed at the same time are captured on streams of their own.
 """
 from __future__ import annotations
 

@@ -15,6 +15,7 @@
 #include <map>
 #include <mutex>
 #include <utility>
+#include <vector>
 
 #include "../../include/vidattn.h"
 #include "classify.cuh"
@@ -185,6 +186,8 @@ int g_epoch = 0;   // counts vidattn_release calls (internal.h)
 struct Scratch {
   void* ptr = nullptr;
   size_t bytes = 0;
+  bool captured = false;     // a graph holds ptr
+  std::vector<void*> kept;   // outgrown buffers that graphs hold
 };
 std::map<std::pair<int, cudaStream_t>, Scratch> g_scratch;
 
@@ -246,24 +249,42 @@ int ensure_device(int* dev_out) {
   return VIDATTN_OK;
 }
 
+bool capturing(cudaStream_t stream) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &status) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return status != cudaStreamCaptureStatusNone;
+}
+
 // Scratch of at least `bytes` for (dev, stream).  Growing synchronises the
-// stream first, so a buffer still in use by earlier work is never freed.
+// stream first, so a buffer still in use by earlier work is never freed; one
+// that a graph was captured with is kept (until vidattn_release), for the graph
+// may be replayed at any time.
 void* scratch_for(int dev, cudaStream_t stream, size_t bytes) {
   std::lock_guard<std::mutex> lk(g_mu);
   Scratch& s = g_scratch[{dev, stream}];
-  if (s.bytes >= bytes) return s.ptr;
-  if (s.ptr) {
-    if (cudaStreamSynchronize(stream) != cudaSuccess) return nullptr;
-    cudaFree(s.ptr);
-    s.ptr = nullptr;
-    s.bytes = 0;
+  if (s.bytes < bytes) {
+    if (s.ptr) {
+      if (s.captured) {
+        s.kept.push_back(s.ptr);
+      } else {
+        if (cudaStreamSynchronize(stream) != cudaSuccess) return nullptr;
+        cudaFree(s.ptr);
+      }
+      s.ptr = nullptr;
+      s.bytes = 0;
+      s.captured = false;
+    }
+    size_t want = bytes < 4096 ? 4096 : bytes;
+    if (cudaMalloc(&s.ptr, want) != cudaSuccess) {
+      s.ptr = nullptr;
+      return nullptr;
+    }
+    s.bytes = want;
   }
-  size_t want = bytes < 4096 ? 4096 : bytes;
-  if (cudaMalloc(&s.ptr, want) != cudaSuccess) {
-    s.ptr = nullptr;
-    return nullptr;
-  }
-  s.bytes = want;
+  if (!s.captured) s.captured = capturing(stream);
   return s.ptr;
 }
 
@@ -1096,10 +1117,11 @@ VIDATTN_API void vidattn_release(void) {
     }
   }
   for (auto& kv : g_scratch) {
-    if (kv.second.ptr) {
+    if (kv.second.ptr || !kv.second.kept.empty()) {
       cudaSetDevice(kv.first.first);
       cudaStreamSynchronize(kv.first.second);
       cudaFree(kv.second.ptr);
+      for (void* p : kv.second.kept) cudaFree(p);
     }
   }
   g_scratch.clear();
